@@ -347,6 +347,113 @@ int moe_block_dots_routine(const uint8_t *packed, int64_t rows, int cols, int wb
  * outputs unspecified. */
 int moe_get_device_error(void *workspace, void *stream, int32_t *code);
 
+/* ---------------------------------------------------------------------------
+ * Dense int8 operators: the parts of the model that are not routed (the first
+ * layers' feed-forward, the attention's projections), which the engine keeps
+ * resident at int8 ([GN] §구현된 주요 기능: int8 rows with per-row scales,
+ * integer-dot kernel).  Weights are rows of int8 codes with one fp32 scale
+ * each, as moe_pack_weights / moe_requant_fp8 write them at wbits 8;
+ * activations are rows of int8 codes with one fp32 scale for each token, as
+ * moe_quantize_act_token writes them.
+ *
+ * For all of them: matrices are row-major with a row stride in ELEMENTS (ld*,
+ * at least the row's length; what lies between the rows is neither read nor
+ * written); any number of rows and columns is supported within the limits
+ * below, and any alignment that fits the element type (rows whose address or
+ * stride is no multiple of 16 bytes take plain loads instead of TMA).
+ * T = 0 returns MOE_OK (gradients that sum over tokens are then set to zero).
+ * T up to 2^28, contractions (cols; in a backward pass the number of matrices
+ * times rows) up to 131071, so that every int32 sum is exact, else
+ * MOE_EUNSUPPORTED.  The current device must be the one that holds the data.
+ * Results do not depend on timing: equal calls give equal bits on one device.
+ * ------------------------------------------------------------------------- */
+enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 }; /* element types */
+/* Activations of the gated block, act(g) = g sigmoid(z): z = g (SiLU), or
+ * z = 2 sqrt(2/pi) (g + 0.044715 g^3) (GELU in its tanh form). */
+enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1 };
+
+/* Per-token quantiser.  For each row of x [n_rows][cols] (elements of type
+ * dtype): d = amax/127 (fp32 IEEE divide), q = round-half-away-from-zero(x *
+ * (1/d)) in [-127, 127]; a row with amax below 2^-112 stores d = 0, q = 0, and
+ * a row that holds an infinity or a NaN stores d = NaN, q = 0.  Outputs
+ * q [n_rows][cols] int8 (row stride ldq) and d [n_rows]. */
+int moe_quantize_act_token(const void *x, int dtype, int64_t n_rows, int cols, int64_t ldx, int8_t *q, int64_t ldq,
+                           float *d, void *stream);
+
+/* Integer product with scales for each token and channel:
+ *   acc[t][n] = sum_k xq[t][k] * w[n][k]              (int32, exact)
+ *   out[t][n] = acc[t][n] * (xd[t] * s[n]) + bias[n]  (fp32, rounded once to dtype)
+ * for xq [T][cols], w [rows][cols], s [rows], bias [rows] or NULL.  acc
+ * [T][rows] (dense) receives the integer sums for moe_int8_matmul_backward;
+ * NULL leaves them out. */
+int moe_int8_matmul(const int8_t *xq, int64_t ldx, const float *xd, int T, const uint8_t *w, int64_t ldw,
+                    const float *s, int rows, int cols, const float *bias, void *out, int dtype, int64_t ldo,
+                    int32_t *acc, void *stream);
+
+/* Gated feed-forward block, both projections, the activation and the product
+ * in one kernel:
+ *   g = acc_gate * (xd s_gate), u = acc_up * (xd s_up)
+ *   out[t][i] = act(g) * u                            (fp32, rounded once to dtype)
+ * with the sums of moe_int8_matmul over w_gate and w_up [rows][cols].  acc
+ * [2][T][rows] (gate, then up) receives the integer sums for
+ * moe_gated_ffn_backward; NULL leaves them out. */
+int moe_gated_ffn(const int8_t *xq, int64_t ldx, const float *xd, int T, const uint8_t *w_gate, int64_t ldg,
+                  const float *s_gate, const uint8_t *w_up, int64_t ldu, const float *s_up, int rows, int cols,
+                  int act, void *out, int dtype, int64_t ldo, int32_t *acc, void *stream);
+
+/* Bytes of device workspace of the backward passes, with n_mats = 1 for
+ * moe_int8_matmul_backward and 2 for moe_gated_ffn_backward (0 when an
+ * argument is out of range). */
+size_t moe_int8_backward_workspace_bytes(int n_mats, int T, int rows, int dtype);
+
+/* Backward pass of moe_int8_matmul for dy [T][rows] (type dtype).  The codes
+ * are constants; gradients reach the dequantised activations x = xd * xq, the
+ * row scales and the bias:
+ *   dx[t][k] = sum_n dy[t][n] s[n] w[n][k]  (type dtype)
+ *   ds[n] = sum_t dy[t][n] xd[t] acc[t][n],  dbias[n] = sum_t dy[t][n]  (fp32)
+ * ds and dbias may be NULL; acc and xd are needed for ds only (NULL
+ * otherwise).  The rows dy s are written as fixed-point numbers of 15 bits and
+ * a sign relative to the row's largest (23 bits for fp32) and multiplied
+ * exactly; a row with an infinity or a NaN gives NaN in its row of dx.
+ * workspace: >= moe_int8_backward_workspace_bytes(1, T, rows, dtype) bytes,
+ * 256-byte aligned; nothing in it is kept between calls. */
+int moe_int8_matmul_backward(const void *dy, int dtype, int64_t lddy, const int32_t *acc, const float *xd, int T,
+                             const uint8_t *w, int64_t ldw, const float *s, int rows, int cols, void *dx,
+                             int64_t lddx, float *ds, float *dbias, void *workspace, size_t ws_bytes, void *stream);
+
+/* Backward pass of moe_gated_ffn for dh [T][rows] (type dtype), from the sums
+ * acc that the forward saved:
+ *   dg = dh u act'(g),  du = dh act(g)
+ *   dx[t][k] = sum_i dg[t][i] s_gate[i] w_gate[i][k] + du[t][i] s_up[i] w_up[i][k]  (type dtype)
+ *   ds_gate[i] = sum_t dg xd[t] acc_gate,  ds_up[i] = sum_t du xd[t] acc_up        (fp32)
+ * ds_gate and ds_up may both be NULL.  Precision and workspace as for
+ * moe_int8_matmul_backward, with n_mats 2. */
+int moe_gated_ffn_backward(const void *dh, int dtype, int64_t lddh, const int32_t *acc, const float *xd, int T,
+                           const uint8_t *w_gate, int64_t ldg, const float *s_gate, const uint8_t *w_up,
+                           int64_t ldu, const float *s_up, int rows, int cols, int act, void *dx, int64_t lddx,
+                           float *ds_gate, float *ds_up, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of device workspace that moe_dense_ffn needs for T tokens (0 when an
+ * argument is out of range). */
+size_t moe_dense_ffn_workspace_bytes(int T, int hidden, int inter);
+
+/* A dense feed-forward over int8 rows, the run of the operators above:
+ *   out = matmul(quantise(gated(quantise(x))))
+ * x and out [T][hidden] of type dtype; the hidden values between are fp32.
+ * experts holds one expert's int8 rows in the layout of moe_experts
+ * (w_gate, w_up [inter][hidden], w_down [hidden][inter]).  workspace: >=
+ * moe_dense_ffn_workspace_bytes(T, hidden, inter) bytes, 256-byte aligned;
+ * nothing in it is kept between calls. */
+int moe_dense_ffn(const void *x, int dtype, int64_t ldx, int T, int hidden, int inter, const moe_experts *experts,
+                  int act, void *out, int64_t ldo, void *workspace, size_t ws_bytes, void *stream);
+
+/* Synchronises `stream`, reads the fault code that a dense product recorded on
+ * the current device since the last read (0 = none, 2 = a device-side wait ran
+ * out; every wait is bounded by the GPU's global timer, 100 ms a pipeline
+ * stage) into *code and clears it.  Returns MOE_OK when it is 0, MOE_EDEVICE
+ * otherwise. */
+int moe_dense_device_error(void *stream, int32_t *code);
+
 /* Test hook of the failure-detection tests (the pages have no counterpart).
  * With withhold_entry >= 0, every following fused small-batch forward
  * (T <= 4) issued by this process skips the publication of the h codes of

@@ -1,0 +1,167 @@
+// moe_dense.cuh -- what the dense int8 operators share: element types, the
+// gated block's activations and their derivatives, the fixed-point planes of a
+// gradient row, and the parameters of the kernels in moe_dense_*.cu.
+//
+// The operators are the dense counterpart of the routed experts' integer-dot
+// matmuls (GeekNews "Show HN: 느린 컴퓨터에서 GLM 5.2 실행하기", §구현된 주요 기능:
+// int8 rows with per-row scales times int8 activations; the engine keeps its
+// dense parts resident at int8): one scale for each token and one for each
+// weight row, so the integer sum runs over the whole row and is scaled once.
+#pragma once
+
+#include <cfloat>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "moe_internal.h"
+
+namespace moe {
+namespace dense {
+
+constexpr int kMaxMats = 2;
+
+// ---------------------------------------------------------------------------
+// Element types of activations, results and gradients (MOE_F32 / BF16 / F16)
+// ---------------------------------------------------------------------------
+template <int DT>
+struct Elem;
+template <>
+struct Elem<MOE_F32> {
+    using T = float;
+};
+template <>
+struct Elem<MOE_BF16> {
+    using T = __nv_bfloat16;
+};
+template <>
+struct Elem<MOE_F16> {
+    using T = __half;
+};
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+// One result element, rounded once to its type.
+__device__ __forceinline__ void store_elem(void* out, int64_t i, int dtype, float v) {
+    if (dtype == MOE_F32)
+        static_cast<float*>(out)[i] = v;
+    else if (dtype == MOE_BF16)
+        static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+    else
+        static_cast<__half*>(out)[i] = __float2half_rn(v);
+}
+
+// ---------------------------------------------------------------------------
+// act(g) = g sigmoid(z(g)): z = g (SiLU), z = 2 sqrt(2/pi)(g + 0.044715 g^3)
+// (the tanh form of GELU, since (1 + tanh y)/2 = sigmoid(2 y); written so, it
+// does not cancel for negative g).  With e = exp(-|z|) <= 1 nothing overflows:
+// sigmoid(z) is 1/(1+e) or e/(1+e), and its derivative e/(1+e)^2.
+// ---------------------------------------------------------------------------
+constexpr float kGelu0 = 1.5957691216057308f;  // 2 sqrt(2/pi)
+constexpr float kGelu1 = 0.044715f;
+
+__device__ __forceinline__ float act_value(int act, float g) {
+    const float z = act == MOE_ACT_SILU ? g : kGelu0 * (g + kGelu1 * g * g * g);
+    const float e = expf(-fabsf(z));
+    const float r = __fdiv_rn(1.0f, 1.0f + e);
+    return g * (z >= 0.0f ? r : e * r);
+}
+
+__device__ __forceinline__ void act_value_grad(int act, float g, float& a, float& da) {
+    const float z = act == MOE_ACT_SILU ? g : kGelu0 * (g + kGelu1 * g * g * g);
+    const float dz = act == MOE_ACT_SILU ? 1.0f : kGelu0 * (1.0f + 3.0f * kGelu1 * g * g);
+    const float e = expf(-fabsf(z));
+    const float r = __fdiv_rn(1.0f, 1.0f + e);
+    const float sig = z >= 0.0f ? r : e * r;
+    const float dsig = e * r * r;
+    a = g * sig;
+    // far out the derivative of the sigmoid is zero while dz may be infinite
+    da = sig + (dsig == 0.0f ? 0.0f : g * dsig * dz);
+}
+
+// ---------------------------------------------------------------------------
+// Fixed-point planes of a gradient row.  A row v with m = max|v| is written as
+// the integers round(v D / m), D = 127 (256^P - 1) / 255 of P signed base-256
+// digits with the top one in [-127, 127], so that
+//   sum_n v_n w_n = (m / D) sum_p 256^p (digit_p . w)
+// runs as P int8 products against the packed weight rows as they lie, each
+// exact in int32.  The only rounding is the one to the row's fixed point: at
+// most m / (2 D) for an element (m 2^-16 for P = 2, m 2^-24 for P = 3).
+// Two planes serve 16-bit gradients (bf16 keeps 8 significant bits, fp16 11,
+// and the sum's error stays below half a step of the result), three fp32.
+// ---------------------------------------------------------------------------
+constexpr int planes_of(int dtype) { return dtype == MOE_F32 ? 3 : 2; }
+template <int P>
+constexpr float kPlaneMax = P == 2 ? 32639.0f : 8355711.0f;
+
+// A row scale: value = integer * a * b (b a power of two that keeps a normal
+// when the row is tiny).
+struct RowScale {
+    float a, b;
+};
+
+// ---------------------------------------------------------------------------
+// The tiled product kernel (moe_dense_gemm.cu)
+// ---------------------------------------------------------------------------
+enum GemmMode { kMatmul = 0, kGated = 1, kGrad = 2 };
+
+struct GemmArgs {
+    // weights: n_mats matrices [rows][cols] of int8, row strides ldw
+    const uint8_t* w[kMaxMats];
+    int64_t ldw[kMaxMats];
+    int n_mats;
+    int rows, cols;
+    // forward: codes [T][cols], row stride ldx.  gradient: planes
+    // [planes][T][ldx], matrix m's part at byte m * mat_pitch of a row
+    const int8_t* x;
+    int64_t ldx;
+    int T;
+    int planes;
+    int64_t mat_pitch;
+    const float* xd;         // forward: token scales
+    const float* s[kMaxMats];  // forward: row scales
+    const float* bias;       // matmul only, may be null
+    const RowScale* gscale;  // gradient: row scales of the planes
+    int act;
+    void* out;
+    int64_t ldo;
+    int dtype;
+    int32_t* acc;  // forward: integer sums [n_mats][T][rows], or null
+};
+
+cudaError_t launch_matmul(const GemmArgs& a, cudaStream_t s);
+cudaError_t launch_gated(const GemmArgs& a, cudaStream_t s);
+cudaError_t launch_grad_matmul(const GemmArgs& a, cudaStream_t s);
+cudaError_t read_device_error(cudaStream_t s, int32_t* code);
+
+// ---------------------------------------------------------------------------
+// Row kernels (moe_dense_rows.cu)
+// ---------------------------------------------------------------------------
+cudaError_t launch_quantize_token(const void* x, int dtype, int64_t rows, int cols, int64_t ldx, int8_t* q,
+                                  int64_t ldq, float* d, cudaStream_t s);
+
+struct GradRowsArgs {
+    const void* dy;  // [T][N]
+    int64_t lddy;
+    int dtype;
+    const int32_t* acc;  // [n_mats][T][N]; may be null for one matrix (no scale gradient)
+    const float* xd;     // [T]; null with acc
+    const float* s[kMaxMats];
+    int n_mats;
+    int T, N;
+    int act;
+    int8_t* planes;  // [P][T][n_mats * pitch]
+    int64_t pitch;
+    RowScale* scale;   // [T]
+    float* partials;   // [grid][2][N] column sums
+    float* colsum[2];  // gated: ds_gate, ds_up; matmul: ds, dbias (each may be null)
+};
+int grad_rows_grid(int T);
+cudaError_t launch_grad_rows(const GradRowsArgs& a, cudaStream_t s);
+
+}  // namespace dense
+}  // namespace moe

@@ -63,6 +63,19 @@ _SIGS = {
     "moe_workspace_view": ([ctypes.POINTER(MoeConfig), _int, _vp, _sz, ctypes.POINTER(MoeWorkspaceLayout)], _int),
     "moe_block_dots": ([_vp, _i64, _int, _int, _vp, _int, _vp, _vp], _int),
     "moe_block_dots_routine": ([_vp, _i64, _int, _int, _vp, _int, _int, _vp, _vp], _int),
+    "moe_quantize_act_token": ([_vp, _int, _i64, _int, _i64, _vp, _i64, _vp, _vp], _int),
+    "moe_int8_matmul": ([_vp, _i64, _vp, _int, _vp, _i64, _vp, _int, _int, _vp, _vp, _int, _i64, _vp, _vp], _int),
+    "moe_gated_ffn": ([_vp, _i64, _vp, _int, _vp, _i64, _vp, _vp, _i64, _vp, _int, _int, _int, _vp, _int, _i64, _vp,
+                       _vp], _int),
+    "moe_int8_backward_workspace_bytes": ([_int, _int, _int, _int], _sz),
+    "moe_int8_matmul_backward": ([_vp, _int, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _int, _vp, _i64, _vp, _vp,
+                                  _vp, _sz, _vp], _int),
+    "moe_gated_ffn_backward": ([_vp, _int, _i64, _vp, _vp, _int, _vp, _i64, _vp, _vp, _i64, _vp, _int, _int, _int,
+                                _vp, _i64, _vp, _vp, _vp, _sz, _vp], _int),
+    "moe_dense_ffn_workspace_bytes": ([_int, _int, _int], _sz),
+    "moe_dense_ffn": ([_vp, _int, _i64, _int, _int, _int, ctypes.POINTER(MoeExperts), _int, _vp, _i64, _vp, _sz,
+                       _vp], _int),
+    "moe_dense_device_error": ([_vp, ctypes.POINTER(ctypes.c_int32)], _int),
     "moe_get_device_error": ([_vp, _vp, ctypes.POINTER(ctypes.c_int32)], _int),
     "moe_noalloc_device_error": ([_vp, ctypes.POINTER(ctypes.c_int32)], _int),
     "moe_synth_normal": ([_u64, _u64, _i64, _i64, _flt, _vp, _vp], _int),
@@ -340,6 +353,232 @@ def synth_bank(wl: synth.Workload, device, shared: bool = False, experts=None) -
             synth_normal(wl.seed, synth.expert_tid(shape, e, m, shared), rows * cols, 0.02, out=buf)
             pack_weights(buf.view(rows, cols), shape.wbits, dst_w[slot], dst_s[slot])
     return bank
+
+
+# ----------------------------------------------------------------------------
+# Dense int8 operators
+#
+# Activations are rows of int8 codes with one fp32 scale for each token, weights
+# rows of int8 codes (uint8 or int8 storage, as pack_weights(w, 8) gives them)
+# with one fp32 scale each.  Matrices may be views whose rows are dense (last
+# stride 1) at any row stride.  The tensors of a call live on one device, which
+# need not be the current one; memory that a call allocates (results and
+# workspace) belongs to the stream that it runs on.
+# ----------------------------------------------------------------------------
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_ACTS = {"silu": 0, "gelu": 1}
+_CODE_TYPES = (torch.int8, torch.uint8)
+_ROW_TYPES = tuple(_DTYPES)
+
+
+def _matrix(t: torch.Tensor, dtypes, name: str, shape=None, device=None) -> int:
+    """Checks a 2-D operand; returns its row stride in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {(rows, cols)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name} must have dense rows (last stride 1) that do not overlap")
+    return ld
+
+
+def _vector(t: torch.Tensor, n: int, name: str, device) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a dense fp32 vector of {n} values")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+
+
+def _sums(acc: torch.Tensor, shape, device) -> None:
+    if (not isinstance(acc, torch.Tensor) or acc.dtype != torch.int32 or tuple(acc.shape) != shape
+            or not acc.is_contiguous() or acc.device != device):
+        raise ValueError(f"acc must be the contiguous int32 sums {shape} that the forward saved, on {device}")
+
+
+def _choice(value, table, name):
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} must be one of {', '.join(str(k) for k in table)}, got {value!r}") from None
+
+
+class _On:
+    """The call's device and stream as the current ones, so that its
+    allocations belong to the stream that uses them."""
+
+    def __init__(self, device: torch.device, stream):
+        self.contexts = []
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the call's tensors on {device}")
+        if device.index != torch.cuda.current_device():
+            self.contexts.append(torch.cuda.device(device))
+        if stream is not None:
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return _stream()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def quantize_act_token(x: torch.Tensor, stream=None):
+    """Rows of x [T][K] (fp32, bf16 or fp16) -> codes [T][K] int8 and scales [T]
+    fp32 (see moe_quantize_act_token)."""
+    ld = _matrix(x, _ROW_TYPES, "x")
+    T, K = x.shape
+    with _On(x.device, stream) as s:
+        q = torch.empty((T, K), dtype=torch.int8, device=x.device)
+        d = torch.empty(T, dtype=torch.float32, device=x.device)
+        _check(lib().moe_quantize_act_token(_ptr(x), _DTYPES[x.dtype], T, K, ld, _ptr(q), K, _ptr(d), s),
+               "quantize_act_token")
+    return q, d
+
+
+def _result(out, T, N, dtype, device):
+    if out is None:
+        return torch.empty((T, N), dtype=dtype, device=device), N
+    return out, _matrix(out, (dtype,), "out", (T, N), device)
+
+
+def int8_matmul(xq: torch.Tensor, xd: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
+                bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+                out: torch.Tensor | None = None, save: bool = False, stream=None):
+    """(xq @ w.T) * xd[:, None] * s + bias: codes xq [T][K] with token scales xd
+    [T], weight codes w [N][K] with row scales s [N] -> [T][N] of out_dtype.
+    save=True also returns the int32 sums [T][N] that the backward pass reads."""
+    ldx, ldw = _matrix(xq, (torch.int8,), "xq"), _matrix(w, _CODE_TYPES, "w")
+    (T, K), N, dev = xq.shape, w.shape[0], xq.device
+    _matrix(w, _CODE_TYPES, "w", (N, K), dev)
+    _vector(xd, T, "xd", dev)
+    _vector(s, N, "s", dev)
+    if bias is not None:
+        _vector(bias, N, "bias", dev)
+    dt = _choice(out_dtype, _DTYPES, "out_dtype")
+    with _On(dev, stream) as st:
+        y, ldo = _result(out, T, N, out_dtype, dev)
+        acc = torch.empty((T, N), dtype=torch.int32, device=dev) if save else None
+        _check(lib().moe_int8_matmul(_ptr(xq), ldx, _ptr(xd), T, _ptr(w), ldw, _ptr(s), N, K, _ptr(bias), _ptr(y), dt,
+                                     ldo, _ptr(acc), st), "int8_matmul")
+    return (y, acc) if save else y
+
+
+def int8_matmul_backward(dy: torch.Tensor, acc: torch.Tensor | None, xd: torch.Tensor | None, w: torch.Tensor,
+                         s: torch.Tensor, bias_grad: bool = False, stream=None):
+    """Gradients of int8_matmul for dy [T][N]: dx [T][K] (of dy's type, with
+    respect to the dequantised activations xd * xq), ds [N] and dbias [N] (fp32).
+    acc=None leaves ds out (None), bias_grad=False dbias."""
+    lddy, ldw = _matrix(dy, _ROW_TYPES, "dy"), _matrix(w, _CODE_TYPES, "w", device=dy.device)
+    (T, N), K, dev = dy.shape, w.shape[1], dy.device
+    if w.shape[0] != N:
+        raise ValueError(f"w must have {N} rows, one for each column of dy, got {w.shape[0]}")
+    _vector(s, N, "s", dev)
+    if acc is not None:
+        _sums(acc, (T, N), dev)
+        _vector(xd, T, "xd", dev)
+    dt = _DTYPES[dy.dtype]
+    with _On(dev, stream) as st:
+        dx = torch.empty((T, K), dtype=dy.dtype, device=dev)
+        ds = torch.empty(N, dtype=torch.float32, device=dev) if acc is not None else None
+        db = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
+        ws = torch.empty(lib().moe_int8_backward_workspace_bytes(1, T, N, dt), dtype=torch.uint8, device=dev)
+        _check(lib().moe_int8_matmul_backward(_ptr(dy), dt, lddy, _ptr(acc), _ptr(xd if acc is not None else None), T,
+                                              _ptr(w), ldw, _ptr(s), N, K, _ptr(dx), K, _ptr(ds), _ptr(db), _ptr(ws),
+                                              ws.numel(), st), "int8_matmul_backward")
+    return dx, ds, db
+
+
+def gated_ffn(xq: torch.Tensor, xd: torch.Tensor, w_gate: torch.Tensor, s_gate: torch.Tensor, w_up: torch.Tensor,
+              s_up: torch.Tensor, act: str = "silu", out_dtype: torch.dtype = torch.float32,
+              out: torch.Tensor | None = None, save: bool = False, stream=None):
+    """act(g) * u with g, u the products of int8_matmul with w_gate and w_up
+    [N][K], in one kernel; act is "silu" or "gelu" (tanh form) -> [T][N] of
+    out_dtype.  save=True also returns the int32 sums [2][T][N] (gate, up) that
+    the backward pass reads."""
+    ldx = _matrix(xq, (torch.int8,), "xq")
+    (T, K), dev = xq.shape, xq.device
+    ldg = _matrix(w_gate, _CODE_TYPES, "w_gate", device=dev)
+    N = w_gate.shape[0]
+    _matrix(w_gate, _CODE_TYPES, "w_gate", (N, K), dev)
+    ldu = _matrix(w_up, _CODE_TYPES, "w_up", (N, K), dev)
+    _vector(xd, T, "xd", dev)
+    _vector(s_gate, N, "s_gate", dev)
+    _vector(s_up, N, "s_up", dev)
+    dt, ac = _choice(out_dtype, _DTYPES, "out_dtype"), _choice(act, _ACTS, "act")
+    with _On(dev, stream) as st:
+        h, ldo = _result(out, T, N, out_dtype, dev)
+        acc = torch.empty((2, T, N), dtype=torch.int32, device=dev) if save else None
+        _check(lib().moe_gated_ffn(_ptr(xq), ldx, _ptr(xd), T, _ptr(w_gate), ldg, _ptr(s_gate), _ptr(w_up), ldu,
+                                   _ptr(s_up), N, K, ac, _ptr(h), dt, ldo, _ptr(acc), st), "gated_ffn")
+    return (h, acc) if save else h
+
+
+def gated_ffn_backward(dh: torch.Tensor, acc: torch.Tensor, xd: torch.Tensor, w_gate: torch.Tensor,
+                       s_gate: torch.Tensor, w_up: torch.Tensor, s_up: torch.Tensor, act: str = "silu",
+                       stream=None):
+    """Gradients of gated_ffn for dh [T][N], from the sums acc [2][T][N] that the
+    forward saved: dx [T][K] (of dh's type, with respect to the dequantised
+    activations xd * xq), ds_gate [N] and ds_up [N] (fp32)."""
+    lddh = _matrix(dh, _ROW_TYPES, "dh")
+    (T, N), dev = dh.shape, dh.device
+    ldg = _matrix(w_gate, _CODE_TYPES, "w_gate", device=dev)
+    K = w_gate.shape[1]
+    _matrix(w_gate, _CODE_TYPES, "w_gate", (N, K), dev)
+    ldu = _matrix(w_up, _CODE_TYPES, "w_up", (N, K), dev)
+    _sums(acc, (2, T, N), dev)
+    _vector(xd, T, "xd", dev)
+    _vector(s_gate, N, "s_gate", dev)
+    _vector(s_up, N, "s_up", dev)
+    dt, ac = _DTYPES[dh.dtype], _choice(act, _ACTS, "act")
+    with _On(dev, stream) as st:
+        dx = torch.empty((T, K), dtype=dh.dtype, device=dev)
+        dsg = torch.empty(N, dtype=torch.float32, device=dev)
+        dsu = torch.empty(N, dtype=torch.float32, device=dev)
+        ws = torch.empty(lib().moe_int8_backward_workspace_bytes(2, T, N, dt), dtype=torch.uint8, device=dev)
+        _check(lib().moe_gated_ffn_backward(_ptr(dh), dt, lddh, _ptr(acc), _ptr(xd), T, _ptr(w_gate), ldg,
+                                            _ptr(s_gate), _ptr(w_up), ldu, _ptr(s_up), N, K, ac, _ptr(dx), K,
+                                            _ptr(dsg), _ptr(dsu), _ptr(ws), ws.numel(), st), "gated_ffn_backward")
+    return dx, dsg, dsu
+
+
+def dense_ffn(x: torch.Tensor, bank: ExpertBank, act: str = "silu", out: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """A dense gated feed-forward over one expert's int8 rows (a bank of one,
+    packed at wbits 8): matmul(quantise(gated(quantise(x)))), x [T][hidden] fp32,
+    bf16 or fp16 -> the same shape and type."""
+    ldx = _matrix(x, _ROW_TYPES, "x")
+    (T, H), dev = x.shape, x.device
+    I = bank.w_gate.shape[1]
+    for name, t, shape in (("w_gate", bank.w_gate, (1, I, H)), ("w_up", bank.w_up, (1, I, H)),
+                           ("w_down", bank.w_down, (1, H, I)), ("s_gate", bank.s_gate, (1, I)),
+                           ("s_up", bank.s_up, (1, I)), ("s_down", bank.s_down, (1, H))):
+        want = torch.float32 if name[0] == "s" else torch.uint8
+        if t.dtype != want or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"bank.{name} must be a contiguous {want} tensor {shape} on {dev} (one int8 expert)")
+    dt, ac = _DTYPES[x.dtype], _choice(act, _ACTS, "act")
+    with _On(dev, stream) as st:
+        y, ldo = _result(out, T, H, x.dtype, dev)
+        ws = torch.empty(lib().moe_dense_ffn_workspace_bytes(T, H, I), dtype=torch.uint8, device=dev)
+        _check(lib().moe_dense_ffn(_ptr(x), dt, ldx, T, H, I, ctypes.byref(bank.struct()), ac, _ptr(y), ldo, _ptr(ws),
+                                   ws.numel(), st), "dense_ffn")
+    return y
+
+
+def dense_device_error(stream=None) -> int:
+    """The fault code that a dense product recorded on the current device (0 =
+    none), cleared by reading; synchronises the stream."""
+    code = ctypes.c_int32(0)
+    st = lib().moe_dense_device_error(_stream(stream), ctypes.byref(code))
+    if st not in (MOE_OK, MOE_EDEVICE):
+        _check(st, "dense_device_error")
+    return code.value
 
 
 # ----------------------------------------------------------------------------

@@ -1,0 +1,109 @@
+"""The dense int8 operators on the GPU against their formulas in 64 bits
+(bounds derived in dense_helpers.py).  Integer sums and codes are exact."""
+import numpy as np
+import pytest
+import torch
+
+import dense_helpers as dh
+from quantized_routed_expert_group_b200 import moe
+
+pytestmark = pytest.mark.gpu
+
+DT = dh.DTYPES
+# tokens, cols, rows: one of everything, sizes around the tiles (16, 32, 64, 128 tokens, 128 rows, 128 codes),
+# odd ones whose rows are no multiple of 16, 8 or 4 bytes, long rows
+SIZES = [(1, 1, 1), (1, 16, 1), (1, 6144, 300), (2, 127, 5), (3, 129, 130), (4, 512, 128), (5, 2048, 257),
+         (16, 1000, 77), (17, 128, 384), (33, 100, 64), (64, 1040, 129), (65, 36, 127), (128, 256, 128),
+         (129, 260, 131), (300, 1000, 500), (257, 1536, 640)]
+LARGE = [(700, 2048, 1500), (1030, 1024, 520), (513, 272, 1032)]
+
+
+def cuda(*ts):
+    return [t.cuda() for t in ts]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("T,K", [(1, 1), (1, 6144), (3, 33), (5, 1000), (64, 2048), (7, 4104), (2, 20000), (2, 70001)])
+def test_quantize_token(T, K, dtype):
+    gen = torch.Generator().manual_seed(T * 7 + K)
+    x = torch.randn((T, K), generator=gen) * torch.exp(2 * torch.randn((T, 1), generator=gen))
+    if K > 8:
+        x[0, :8] = torch.tensor([0.5, -0.5, 1.5, -1.5, 2.5, -2.5, 63.5, 127.0])  # ties: the scale is 1
+        x[0, 8:] = 0
+    if T > 2:
+        x[1] = 0
+        x[2] = 1e-36 if dtype != "fp16" else 0.0
+    x = x.to(DT[dtype])
+    q, d = moe.quantize_act_token(x.cuda())
+    xn = x.float().numpy()
+    amax = np.abs(xn).max(1)
+    live = amax >= np.float32(2.0 ** -112)
+    want_d = np.where(live, amax / np.float32(127), np.float32(0)).astype(np.float32)
+    inv = np.where(live, np.float32(1) / np.where(live, want_d, np.float32(1)), np.float32(0)).astype(np.float32)
+    v = (xn * inv[:, None]).astype(np.float32)
+    want_q = np.clip(np.sign(v) * np.floor(np.abs(v).astype(np.float64) + 0.5), -127, 127).astype(np.int8)
+    np.testing.assert_array_equal(d.cpu().numpy().view(np.uint32), want_d.view(np.uint32))
+    np.testing.assert_array_equal(q.cpu().numpy(), want_q)
+
+
+def test_quantize_token_non_finite_rows():
+    x = torch.randn(5, 100)
+    x[1, 3], x[2, 99], x[3, 0] = float("nan"), float("inf"), float("-inf")
+    q, d = moe.quantize_act_token(x.cuda())
+    assert torch.isnan(d.cpu()).tolist() == [False, True, True, True, False]
+    assert not q[1:4].any() and q[0].any() and q[4].any()
+    y = moe.int8_matmul(q, d, torch.ones((3, 100), dtype=torch.int8, device="cuda"), torch.ones(3, device="cuda"))
+    assert torch.isnan(y.cpu()).all(1).tolist() == [False, True, True, True, False]
+
+
+@pytest.mark.parametrize("T,K,N", SIZES + LARGE)
+@pytest.mark.parametrize("dtype", list(DT))
+def test_matmul(T, K, N, dtype):
+    x, xd, (w,), (s,), bias, _ = dh.inputs(T + K + N, T, K, N, 1, DT[dtype])
+    acc, y, tol = dh.ref_matmul(x, xd, w, s, bias, DT[dtype])
+    got, got_acc = moe.int8_matmul(*cuda(x, xd, w, s, bias), out_dtype=DT[dtype], save=True)
+    assert torch.equal(got_acc.cpu().double(), acc)
+    dh.check("y", got, y, tol)
+    _, y, tol = dh.ref_matmul(x, xd, w, s, None, DT[dtype])
+    dh.check("y without bias", moe.int8_matmul(*cuda(x, xd, w.view(torch.uint8), s), out_dtype=DT[dtype]), y, tol)
+    assert moe.dense_device_error() == 0
+
+
+@pytest.mark.parametrize("T,K,N", SIZES + LARGE)
+@pytest.mark.parametrize("act,dtype", [("silu", "fp32"), ("silu", "bf16"), ("gelu", "fp32"), ("gelu", "fp16")])
+def test_gated(T, K, N, act, dtype):
+    x, xd, ws, ss, _, _ = dh.inputs(T + K + N, T, K, N, 2, DT[dtype])
+    acc, h, tol = dh.ref_gated(x, xd, ws, ss, act, DT[dtype])
+    got, got_acc = moe.gated_ffn(*cuda(x, xd, ws[0], ss[0], ws[1], ss[1]), act=act, out_dtype=DT[dtype], save=True)
+    assert torch.equal(got_acc.cpu().double(), acc)
+    dh.check("h", got, h, tol)
+    again = moe.gated_ffn(*cuda(x, xd, ws[0], ss[0], ws[1], ss[1]), act=act, out_dtype=DT[dtype])
+    assert torch.equal(got, again)
+    assert moe.dense_device_error() == 0
+
+
+@pytest.mark.parametrize("T,K,N", SIZES + LARGE)
+@pytest.mark.parametrize("dtype", list(DT))
+def test_matmul_backward(T, K, N, dtype):
+    x, xd, (w,), (s,), _, dy = dh.inputs(T + K + N, T, K, N, 1, DT[dtype])
+    acc = dh.sums64(x, w)
+    refs = dh.ref_matmul_backward(dy, acc, xd, w, s, DT[dtype])
+    c = cuda(dy, acc.int(), xd, w, s)
+    got = moe.int8_matmul_backward(*c, bias_grad=True)
+    for name, g, (want, tol) in zip(("dx", "ds", "dbias"), got, refs):
+        dh.check(name, g, want, tol)
+    dx, ds, db = moe.int8_matmul_backward(c[0], None, None, c[3], c[4])
+    assert ds is None and db is None and torch.equal(dx, got[0])
+    assert moe.dense_device_error() == 0
+
+
+@pytest.mark.parametrize("T,K,N", SIZES + LARGE)
+@pytest.mark.parametrize("act,dtype", [("silu", "fp32"), ("silu", "bf16"), ("gelu", "fp32"), ("gelu", "fp16")])
+def test_gated_backward(T, K, N, act, dtype):
+    x, xd, ws, ss, _, dy = dh.inputs(T + K + N, T, K, N, 2, DT[dtype])
+    acc = torch.stack([dh.sums64(x, w) for w in ws])
+    refs = dh.ref_gated_backward(dy, acc, xd, ws, ss, act, DT[dtype])
+    got = moe.gated_ffn_backward(*cuda(dy, acc.int(), xd, ws[0], ss[0], ws[1], ss[1]), act=act)
+    for name, g, (want, tol) in zip(("dx", "ds_gate", "ds_up"), got, refs):
+        dh.check(name, g, want, tol)
+    assert moe.dense_device_error() == 0
