@@ -369,6 +369,383 @@ __global__ void __launch_bounds__(kTileThreads)
 }
 
 // ---------------------------------------------------------------------------
+// Large batches: CTA pairs, one 256-row MMA over both SMs' shared memory
+// ---------------------------------------------------------------------------
+// A pair of CTAs (cluster of two) works on tiles of 256 x n columns: each CTA
+// holds 128 rows of the MMA's first operand and half of the second operand's
+// rows, so a stage of 128 codes moves 32 KB a CTA for 128 x 256 x 128 products:
+// half of what a CTA alone would load and read for them.  The CTAs are
+// persistent (tiles pair, pair + pairs, ...), and the accumulator is doubled,
+// so a tile's epilogue runs under the next tile's products.
+//   matmul, grad: rows = 256 channels, columns = tokens (times planes): a lane
+//     is a channel, and a warp's stores run along a token's row
+//   gated: rows = 256 tokens, columns = 128 gate and 128 up channels (one half
+//     from each CTA), so that a lane holds a token's g and u of one channel
+constexpr int kPairThreads = 192;
+constexpr int kPairStages = 6;
+constexpr int kPairCtl = 1024 + 4 * 2 * 256 * 8;  // barriers; each epilogue warp's scales of two tiles' columns
+constexpr int kPairSmem = kPairStages * 2 * kTileBytes + kPairCtl + 1024;
+constexpr int kPairRows = 256;
+
+struct PairParams {
+    const float* xd;
+    const float* s[kMaxMats];
+    const float* bias;
+    const RowScale* gscale;
+    void* out;
+    int64_t ldo;
+    int32_t* acc;
+    int64_t mat_pitch;
+    int T, rows, out_rows;
+    int k_steps, steps;
+    int nt;            // matmul, grad: tokens of a tile; gated: channels of a tile
+    int tiles_r;       // tiles along the 256 rows
+    int64_t tiles;
+    int act, dtype;
+    int vec;           // gated: results and sums may be stored 16 bytes at a time
+};
+
+__device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+
+// A box into this CTA's shared memory, completing on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// Arrive on the barrier at this offset in both CTAs when the MMAs issued so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Bounded wait on a barrier that the other CTA arrives on too.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint64_t budget_ns) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity), "r"(64u)
+            : "memory");
+        if (ok) return true;
+        if ((i & 255u) == 0) {
+            const uint64_t t = global_timer_ns();
+            if (i == 0)
+                t0 = t;
+            else if (t - t0 > budget_ns)
+                return false;
+        }
+    }
+}
+
+// Sixteen results of one token, channels n .. n + 15.
+__device__ __forceinline__ void store16(const PairParams& p, int64_t t, int n, const float (&v)[16]) {
+    if (p.vec && n + 16 <= p.out_rows) {
+        if (p.dtype == MOE_F32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + t * p.ldo + n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (p.dtype == MOE_BF16) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + t * p.ldo + n);
+            o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (n + i < p.out_rows) store_elem(p.out, t * p.ldo + n + i, p.dtype, v[i]);
+    }
+}
+
+__device__ __forceinline__ void store_acc16(const PairParams& p, int32_t* row, int n, const uint32_t (&v)[16]) {
+    if (p.vec && n + 16 <= p.out_rows) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4*>(row + n)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (n + i < p.out_rows) row[n + i] = (int)v[i];
+    }
+}
+
+template <int MODE, int P>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    k_dense_pair(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUtensorMap wmap1,
+                 const __grid_constant__ CUtensorMap xmap, const PairParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ctl = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(ctl);
+    uint64_t* empty = full + kPairStages;
+    uint64_t* accf = empty + kPairStages;  // [2]
+    uint64_t* acce = accf + 2;             // [2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
+    uint8_t* sm = ctl + kPairCtl;
+    constexpr int kStage = 2 * kTileBytes;
+
+    uint32_t rank;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ncols = MODE == kGated ? 2 * p.nt : P * p.nt;  // the MMA's N
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accf[b], 1);
+            mbar_init(&acce[b], 8);  // four epilogue warps of each CTA
+        }
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before_sync();
+    cluster_sync_all();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- producer (both CTAs) ----------------
+            tma_prefetch_map(&wmap0);
+            if (MODE != kMatmul) tma_prefetch_map(&wmap1);
+            tma_prefetch_map(&xmap);
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            const uint32_t tx = 2 * (kTileBytes + ncols / 2 * kStageK);  // both CTAs' boxes
+            for (int64_t tile = pair; ok && tile < p.tiles; tile += pairs) {
+                const int r0 = (int)(tile % p.tiles_r) * kPairRows;
+                const int64_t c0 = tile / p.tiles_r * p.nt;
+                for (int ks = 0; ks < p.steps; ++ks) {
+                    if (!wait_cluster(&empty[s], ph ^ 1u, kWaitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
+                    const uint32_t bar = map_rank(&full[s], 0);
+                    uint8_t* st = sm + s * kStage;
+                    if constexpr (MODE == kGrad) {
+                        const int m = ks / p.k_steps, k = (ks - m * p.k_steps) * kStageK;
+                        tma_load_2d_pair(st, m ? &wmap1 : &wmap0, r0 + 128 * rank, k, bar);
+                        const int x = (int)(m * p.mat_pitch) + k;
+                        if constexpr (P == 2) {  // one plane a CTA
+                            tma_load_2d_pair(st + kTileBytes, &xmap, x, (int)((int64_t)rank * p.T + c0), bar);
+                        } else {  // three halves of planes a CTA
+#pragma unroll
+                            for (int j = 0; j < 3; ++j) {
+                                const int h = 3 * rank + j;
+                                tma_load_2d_pair(st + kTileBytes + j * p.nt / 2 * kStageK, &xmap, x,
+                                                 (int)((int64_t)(h >> 1) * p.T + c0 + (h & 1) * (p.nt / 2)), bar);
+                            }
+                        }
+                    } else if constexpr (MODE == kMatmul) {
+                        tma_load_2d_pair(st, &wmap0, ks * kStageK, r0 + 128 * rank, bar);
+                        tma_load_2d_pair(st + kTileBytes, &xmap, ks * kStageK, (int)(c0 + rank * (p.nt / 2)), bar);
+                    } else {
+                        tma_load_2d_pair(st, &xmap, ks * kStageK, r0 + 128 * rank, bar);
+                        tma_load_2d_pair(st + kTileBytes, rank ? &wmap1 : &wmap0, ks * kStageK, (int)c0, bar);
+                    }
+                    if (++s == kPairStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            if (!ok) set_error(&g_dense_error, kErrTimeout);
+            // every box has been consumed before the CTA ends
+            for (int i = 0; i < kPairStages; ++i) {
+                if (!wait_cluster(&empty[s], ph ^ 1u, kWaitNs)) {
+                    set_error(&g_dense_error, kErrTimeout);
+                    break;
+                }
+                if (++s == kPairStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------- MMA issuer (the pair's first CTA) ----------------
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            const uint32_t idesc = (idesc_tile<MODE>(ncols) & ~(31u << 24)) | ((uint32_t)(kPairRows >> 4) << 24);
+            int nu = 0;
+            for (int64_t tile = pair; ok && tile < p.tiles; tile += pairs, ++nu) {
+                const int buf = nu & 1;
+                if (nu >= 2 && !wait_cluster(&acce[buf], ((nu >> 1) - 1) & 1, kWaitNs)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d = tmem + 256 * buf;
+                for (int ks = 0; ks < p.steps; ++ks) {
+                    if (!wait_cluster(&full[s], ph, kWaitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    uint8_t* st = sm + s * kStage;
+                    const uint64_t a0 = MODE == kGrad ? desc_mn128_sw128(st) : desc_k128_sw128(st);
+                    const uint64_t b0 = desc_k128_sw128(st + kTileBytes);
+#pragma unroll
+                    for (int j = 0; j < kStageK / 32; ++j)
+                        mma_i8_pair(d, a0 + (MODE == kGrad ? 256 * j : 2 * j), b0 + 2 * j, idesc, ks > 0 || j > 0);
+                    mma_commit_pair(&empty[s]);
+                    if (++s == kPairStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                mma_commit_pair(&accf[buf]);
+            }
+            if (!ok) set_error(&g_dense_error, kErrTimeout);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- epilogue: warps 2..5 = TMEM lane quarters 2, 3, 0, 1 ----------------
+        const int quad = warp & 3, row = 32 * quad + lane;
+        // a copy for each warp: the epilogue warps never wait for one another
+        RowScale* tok = reinterpret_cast<RowScale*>(ctl + 1024) + quad * 512;
+        int nu = 0;
+        for (int64_t tile = pair; tile < p.tiles; tile += pairs, ++nu) {
+            const int buf = nu & 1;
+            const int64_t r0 = (tile % p.tiles_r) * kPairRows + 128 * rank;
+            const int64_t c0 = tile / p.tiles_r * p.nt;
+            RowScale* ts = tok + 256 * buf;
+            for (int i = lane; i < p.nt; i += 32) {
+                if constexpr (MODE == kGated)
+                    ts[i] = c0 + i < p.rows ? RowScale{p.s[0][c0 + i], p.s[1][c0 + i]} : RowScale{0.0f, 0.0f};
+                else if (c0 + i < p.T)
+                    ts[i] = MODE == kGrad ? p.gscale[c0 + i] : RowScale{p.xd[c0 + i], 1.0f};
+            }
+            float sa = 0.0f, bias = 0.0f;
+            if constexpr (MODE == kGated) {
+                if (r0 + row < p.T) sa = p.xd[r0 + row];
+            } else if constexpr (MODE == kMatmul) {
+                if (r0 + row < p.out_rows) {
+                    sa = p.s[0][r0 + row];
+                    if (p.bias) bias = p.bias[r0 + row];
+                }
+            }
+            // (a whole warp gives up together)
+            if (!__all_sync(kFull, wait_cluster(&accf[buf], (uint32_t)(nu >> 1) & 1u, kWaitAllNs))) {
+                set_error(&g_dense_error, kErrTimeout);
+                break;
+            }
+            tc_fence_after_sync();
+            const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 256 * buf;
+            if constexpr (MODE == kGated) {
+                const int64_t t = r0 + row;
+                for (int c = 0; c < p.nt; c += 16) {
+                    uint32_t g[16], u[16];
+                    tmem_ld16(tl + c, g);
+                    tmem_ld16(tl + p.nt + c, u);
+                    tmem_wait_ld();
+                    if (t < p.T) {
+                        float h[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const RowScale sc = ts[c + j];
+                            h[j] = act_value(p.act, (float)(int)g[j] * (sa * sc.a)) * ((float)(int)u[j] * (sa * sc.b));
+                        }
+                        store16(p, t, (int)c0 + c, h);
+                        if (p.acc) {
+                            store_acc16(p, p.acc + t * p.rows, (int)c0 + c, g);
+                            store_acc16(p, p.acc + (p.T + t) * p.rows, (int)c0 + c, u);
+                        }
+                    }
+                }
+            } else {
+                const int64_t n = r0 + row;
+                const int nv = (int)min((int64_t)p.nt, p.T - c0);
+                for (int c = 0; c < nv; c += 16) {
+                    uint32_t v[P][16];
+#pragma unroll
+                    for (int i = 0; i < P; ++i) tmem_ld16(tl + i * p.nt + c, v[i]);
+                    tmem_wait_ld();
+                    if (n < p.out_rows) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (c + j >= nv) break;
+                            const RowScale sc = ts[c + j];
+                            const int64_t t = c0 + c + j;
+                            float f;
+                            if constexpr (MODE == kGrad) {
+                                f = (float)(int)v[P - 1][j];
+#pragma unroll
+                                for (int i = P - 2; i >= 0; --i) f = fmaf(f, 256.0f, (float)(int)v[i][j]);
+                                f = f * sc.a * sc.b;
+                            } else {
+                                if (p.acc) p.acc[t * p.rows + n] = (int)v[0][j];
+                                f = (float)(int)v[0][j] * (sc.a * sa) + bias;
+                            }
+                            store_elem(p.out, t * p.ldo + n, p.dtype, f);
+                        }
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(map_rank(&acce[buf], 0));
+        }
+    }
+    tc_fence_before_sync();
+    cluster_sync_all();  // neither CTA ends while the other's MMAs or arrivals may still reach it
+    tc_fence_after_sync();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
 static int unit_of(const void* p, int64_t ld) {
@@ -475,11 +852,77 @@ static cudaError_t run_tile(const GemmArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k_dense_tile<MODE, P>, wm[0], wm[1], xm, p);
 }
 
-cudaError_t launch_matmul(const GemmArgs& a, cudaStream_t s) { return run_tile<kMatmul, 1>(a, s); }
+template <int MODE, int P>
+static cudaError_t run_pair(const GemmArgs& a, cudaStream_t s) {
+    static bool attr_done[64];
+    cudaError_t e = allow_smem(k_dense_pair<MODE, P>, attr_done);
+    if (e != cudaSuccess) return e;
+    PairParams p{};
+    p.xd = a.xd;
+    p.s[0] = a.s[0];
+    p.s[1] = a.s[1];
+    p.bias = a.bias;
+    p.gscale = a.gscale;
+    p.out = a.out;
+    p.ldo = a.ldo;
+    p.acc = a.acc;
+    p.mat_pitch = a.mat_pitch;
+    p.T = a.T;
+    p.rows = a.rows;
+    p.out_rows = MODE == kGrad ? a.cols : a.rows;
+    p.k_steps = ((MODE == kGrad ? a.rows : a.cols) + kStageK - 1) / kStageK;
+    p.steps = p.k_steps * (MODE == kGrad ? a.n_mats : 1);
+    p.act = a.act;
+    p.dtype = a.dtype;
+    const int esz = a.dtype == MOE_F32 ? 4 : 2;
+    p.vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ldo * esz % 16 == 0 &&
+            (!a.acc || (reinterpret_cast<uintptr_t>(a.acc) % 16 == 0 && a.rows % 4 == 0));
+    p.nt = MODE == kGated ? 128 : MODE == kMatmul ? 256 : P == 2 ? 128 : 64;
+    p.tiles_r = ((MODE == kGated ? a.T : p.out_rows) + kPairRows - 1) / kPairRows;
+    const int tiles_c = ((MODE == kGated ? a.rows : a.T) + p.nt - 1) / p.nt;
+    p.tiles = (int64_t)p.tiles_r * tiles_c;
+    // boxes of the three operands: the MMA's rows are 128 a CTA, its columns half of the pair's
+    const int wbox = MODE == kGated ? p.nt : 128;
+    const int xbox = MODE == kGated ? 128 : MODE == kMatmul ? p.nt / 2 : P == 2 ? p.nt : p.nt / 2;
+    CUtensorMap wm[kMaxMats], xm;
+    for (int m = 0; m < a.n_mats; ++m) {
+        e = encode_2d(&wm[m], a.w[m], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.cols, a.rows, a.ldw[m], kStageK, wbox,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
+        if (e != cudaSuccess) return e;
+    }
+    if (a.n_mats == 1) wm[1] = wm[0];
+    e = encode_2d(&xm, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, MODE == kGrad ? a.n_mats * a.mat_pitch : a.cols,
+                  (uint64_t)a.planes * a.T, a.ldx, kStageK, xbox, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = device_info().sm_count / 2;
+    const unsigned grid = 2 * (unsigned)(p.tiles < pairs ? p.tiles : pairs);
+    k_dense_pair<MODE, P><<<grid, kPairThreads, kPairSmem, s>>>(wm[0], wm[1], xm, p);
+    return cudaGetLastError();
+}
 
-cudaError_t launch_gated(const GemmArgs& a, cudaStream_t s) { return run_tile<kGated, 1>(a, s); }
+// Whether TMA can take every operand: addresses and row strides on 16 bytes.
+static bool tma_operands(const GemmArgs& a) {
+    bool ok = unit_of(a.x, a.ldx) == 16;
+    for (int m = 0; m < a.n_mats; ++m) ok = ok && unit_of(a.w[m], a.ldw[m]) == 16;
+    return ok;
+}
+
+// Pairs from this many tokens on.
+constexpr int kPairTokens = 256;
+
+cudaError_t launch_matmul(const GemmArgs& a, cudaStream_t s) {
+    if (a.T >= kPairTokens && tma_operands(a)) return run_pair<kMatmul, 1>(a, s);
+    return run_tile<kMatmul, 1>(a, s);
+}
+
+cudaError_t launch_gated(const GemmArgs& a, cudaStream_t s) {
+    if (a.T >= kPairTokens && tma_operands(a)) return run_pair<kGated, 1>(a, s);
+    return run_tile<kGated, 1>(a, s);
+}
 
 cudaError_t launch_grad_matmul(const GemmArgs& a, cudaStream_t s) {
+    if (a.T >= kPairTokens && tma_operands(a))
+        return a.planes == 2 ? run_pair<kGrad, 2>(a, s) : run_pair<kGrad, 3>(a, s);
     return a.planes == 2 ? run_tile<kGrad, 2>(a, s) : run_tile<kGrad, 3>(a, s);
 }
 
