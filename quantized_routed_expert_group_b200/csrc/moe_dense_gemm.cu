@@ -11,7 +11,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <mutex>
+#include <type_traits>
 
 #include "moe_dense.cuh"
 #include "moe_device.cuh"
@@ -365,6 +365,126 @@ __global__ void __launch_bounds__(kTileThreads)
             }
         }
         cluster_sync_all();  // the peers have read this CTA's sums
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A few tokens: integer dots on the CUDA cores
+// ---------------------------------------------------------------------------
+// With up to TN tokens the products stream the weights once and do a few
+// dp4a per loaded word: a row (gated: its gate and up rows) is read by `wpr`
+// warps of one CTA, each lane taking every (32 wpr)-th 16-byte chunk with
+// kUnroll of them in flight, and the warps' sums meet in shared memory.  The
+// tokens' codes come through L1.  More warps share a row when the rows alone do
+// not fill the SMs.
+constexpr int kDotThreads = 256;
+
+struct DotParams {
+    const uint8_t* w[kMaxMats];
+    int64_t ldw[kMaxMats];
+    const uint8_t* x;
+    int64_t ldx;
+    const float* xd;
+    const float* s[kMaxMats];
+    const float* bias;
+    void* out;
+    int64_t ldo;
+    int32_t* acc;
+    int T, rows, cols;
+    int wpr;  // warps of a row: 1, 2, 4 or 8
+    int act, dtype;
+    int w_unit[kMaxMats], x_unit;
+};
+
+__device__ __forceinline__ int dot16(const uint4 a, const uint4 b, int c) {
+    c = __dp4a((int)a.x, (int)b.x, c);
+    c = __dp4a((int)a.y, (int)b.y, c);
+    c = __dp4a((int)a.z, (int)b.z, c);
+    return __dp4a((int)a.w, (int)b.w, c);
+}
+
+// FAST: rows on the 16-byte grid, full chunks read with 16-byte loads.
+template <int MODE, int TN, bool FAST>
+__global__ void __launch_bounds__(kDotThreads) k_dense_dot(const DotParams p) {
+    constexpr int M = MODE == kGated ? 2 : 1;
+    constexpr int kUnroll = FAST ? (TN == 1 ? 6 : TN == 2 ? 4 : 2) : 1;
+    __shared__ int sh[8][M * TN];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rpc = 8 / p.wpr;  // rows of a CTA
+    const int64_t row = (int64_t)blockIdx.x * rpc + warp / p.wpr;
+    const int sub = warp % p.wpr;
+    int v[M][TN];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int t = 0; t < TN; ++t) v[m][t] = 0;
+    if (row < p.rows) {
+        const uint8_t* wr[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m) wr[m] = p.w[m] + row * p.ldw[m];
+        const int chunks = p.cols / 16, step = 32 * p.wpr;
+        int c = lane + 32 * sub;
+        if constexpr (FAST) {
+            for (; c < chunks; c += kUnroll * step) {
+                uint4 a[kUnroll][M];
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                    for (int m = 0; m < M; ++m) {
+                        const int cu = c + u * step;
+                        a[u][m] = cu < chunks ? ld_stream_v4(wr[m] + 16 * (int64_t)cu) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    const int cu = min(c + u * step, chunks - 1);
+#pragma unroll
+                    for (int t = 0; t < TN; ++t) {
+                        const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.x + min(t, p.T - 1) * p.ldx) + cu);
+#pragma unroll
+                        for (int m = 0; m < M; ++m) v[m][t] = dot16(a[u][m], b, v[m][t]);
+                    }
+                }
+            }
+        }
+        // the row's last bytes; the whole row when it is off the grid
+        for (c = FAST ? chunks + lane + 32 * sub : lane + 32 * sub; c * 16 < p.cols; c += step) {
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const uint4 a = load16(wr[m], (int64_t)c * 16, p.cols, p.w_unit[m]);
+#pragma unroll
+                for (int t = 0; t < TN; ++t)
+                    v[m][t] = dot16(a, load16(p.x + min(t, p.T - 1) * p.ldx, (int64_t)c * 16, p.cols, p.x_unit),
+                                    v[m][t]);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+            v[m][t] = __reduce_add_sync(kFull, v[m][t]);
+            if (lane == 0) sh[warp][m * TN + t] = v[m][t];
+        }
+    if (p.wpr > 1)
+        __syncthreads();
+    else
+        __syncwarp();
+    // lane t of a row's first warp joins token t's sums
+    if (sub == 0 && row < p.rows && lane < p.T) {
+        int r[M];
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            r[m] = 0;
+            for (int i = 0; i < p.wpr; ++i) r[m] += sh[warp + i][m * TN + lane];
+            if (p.acc) p.acc[((int64_t)m * p.T + lane) * p.rows + row] = r[m];
+        }
+        const float xd = p.xd[lane];
+        float y = (float)r[0] * (xd * p.s[0][row]);
+        if constexpr (MODE == kGated)
+            y = act_value(p.act, y) * ((float)r[1] * (xd * p.s[1][row]));
+        else if (p.bias)
+            y += p.bias[row];
+        store_elem(p.out, lane * p.ldo + row, p.dtype, y);
     }
 }
 
@@ -907,15 +1027,64 @@ static bool tma_operands(const GemmArgs& a) {
     return ok;
 }
 
-// Pairs from this many tokens on.
+template <int MODE>
+static cudaError_t run_dot(const GemmArgs& a, cudaStream_t s) {
+    DotParams p{};
+    bool fast = true;
+    for (int m = 0; m < a.n_mats; ++m) {
+        p.w[m] = a.w[m];
+        p.ldw[m] = a.ldw[m];
+        p.s[m] = a.s[m];
+        p.w_unit[m] = unit_of(a.w[m], a.ldw[m]);
+        fast = fast && p.w_unit[m] == 16;
+    }
+    p.x = reinterpret_cast<const uint8_t*>(a.x);
+    p.ldx = a.ldx;
+    p.x_unit = unit_of(a.x, a.ldx);
+    fast = fast && p.x_unit == 16;
+    p.xd = a.xd;
+    p.bias = a.bias;
+    p.out = a.out;
+    p.ldo = a.ldo;
+    p.acc = a.acc;
+    p.T = a.T;
+    p.rows = a.rows;
+    p.cols = a.cols;
+    p.act = a.act;
+    p.dtype = a.dtype;
+    // warps enough for 32 on each SM, while a lane has two chunks or more
+    p.wpr = 1;
+    while (p.wpr < 8 && (int64_t)a.rows * p.wpr < 32 * (int64_t)device_info().sm_count &&
+           a.cols / 16 >= 2 * 32 * 2 * p.wpr)
+        p.wpr *= 2;
+    const int rpc = 8 / p.wpr;
+    const unsigned grid = (unsigned)((a.rows + (int64_t)rpc - 1) / rpc);
+    auto go = [&](auto tn) {
+        constexpr int TN = decltype(tn)::value;
+        if (fast)
+            k_dense_dot<MODE, TN, true><<<grid, kDotThreads, 0, s>>>(p);
+        else
+            k_dense_dot<MODE, TN, false><<<grid, kDotThreads, 0, s>>>(p);
+        return cudaGetLastError();
+    };
+    if (a.T == 1) return go(std::integral_constant<int, 1>());
+    if (a.T == 2) return go(std::integral_constant<int, 2>());
+    if (a.T <= 4) return go(std::integral_constant<int, 4>());
+    return go(std::integral_constant<int, 8>());
+}
+
+// Tokens up to which the CUDA-core kernel runs, and from which CTA pairs do.
+constexpr int kDotTokens = 4;
 constexpr int kPairTokens = 256;
 
 cudaError_t launch_matmul(const GemmArgs& a, cudaStream_t s) {
+    if (a.T <= kDotTokens) return run_dot<kMatmul>(a, s);
     if (a.T >= kPairTokens && tma_operands(a)) return run_pair<kMatmul, 1>(a, s);
     return run_tile<kMatmul, 1>(a, s);
 }
 
 cudaError_t launch_gated(const GemmArgs& a, cudaStream_t s) {
+    if (a.T <= kDotTokens) return run_dot<kGated>(a, s);
     if (a.T >= kPairTokens && tma_operands(a)) return run_pair<kGated, 1>(a, s);
     return run_tile<kGated, 1>(a, s);
 }

@@ -367,36 +367,40 @@ def synth_bank(wl: synth.Workload, device, shared: bool = False, experts=None) -
 # ----------------------------------------------------------------------------
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _ACTS = {"silu": 0, "gelu": 1}
+_ACT_TYPES = (torch.int8,)
 _CODE_TYPES = (torch.int8, torch.uint8)
 _ROW_TYPES = tuple(_DTYPES)
 
 
-def _matrix(t: torch.Tensor, dtypes, name: str, shape=None, device=None) -> int:
-    """Checks a 2-D operand; returns its row stride in elements."""
+def _matrix(t: torch.Tensor, dtypes, name: str, rows: int = -1, cols: int = -1, dev: int = -1) -> int:
+    """Checks a 2-D operand (its rows, columns and device where they are given);
+    returns its row stride in elements."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {(rows, cols)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
-    ld = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+    (r, c), (ld, inner) = t.shape, t.stride()
+    if (rows >= 0 and r != rows) or (cols >= 0 and c != cols):
+        want = tuple("any" if n < 0 else n for n in (rows, cols))
+        raise ValueError(f"{name} must have shape {want}, got {(r, c)}")
+    if dev >= 0 and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    if r <= 1:
+        ld = c
+    if (inner != 1 and c > 1) or ld < c:
         raise ValueError(f"{name} must have dense rows (last stride 1) that do not overlap")
     return ld
 
 
-def _vector(t: torch.Tensor, n: int, name: str, device) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+def _vector(t: torch.Tensor, n: int, name: str, dev: int) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a dense fp32 vector of {n} values")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
 
 
-def _sums(acc: torch.Tensor, shape, device) -> None:
-    if (not isinstance(acc, torch.Tensor) or acc.dtype != torch.int32 or tuple(acc.shape) != shape
-            or not acc.is_contiguous() or acc.device != device):
-        raise ValueError(f"acc must be the contiguous int32 sums {shape} that the forward saved, on {device}")
+def _sums(acc: torch.Tensor, shape, dev: int) -> None:
+    if (not isinstance(acc, torch.Tensor) or acc.dtype != torch.int32 or acc.shape != shape
+            or not acc.is_contiguous() or acc.get_device() != dev):
+        raise ValueError(f"acc must be the contiguous int32 sums {shape} that the forward saved, on cuda:{dev}")
 
 
 def _choice(value, table, name):
@@ -406,26 +410,31 @@ def _choice(value, table, name):
         raise ValueError(f"{name} must be one of {', '.join(str(k) for k in table)}, got {value!r}") from None
 
 
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
 class _On:
     """The call's device and stream as the current ones, so that its
-    allocations belong to the stream that uses them."""
+    allocations belong to the stream that uses them; gives the stream's handle."""
+    __slots__ = ("dev", "contexts")
 
-    def __init__(self, device: torch.device, stream):
-        self.contexts = []
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the call's tensors on {device}")
-        if device.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(device))
+    def __init__(self, dev: int, stream):
+        self.dev, self.contexts = dev, ()
         if stream is not None:
-            self.contexts.append(torch.cuda.stream(stream))
+            if stream.device.index != dev:
+                raise ValueError(f"stream is on {stream.device}, the call's tensors on cuda:{dev}")
+            self.contexts = (torch.cuda.stream(stream),)  # also makes its device the current one
+        elif dev != torch.cuda.current_device():
+            self.contexts = (torch.cuda.device(dev),)
 
-    def __enter__(self):
+    def __enter__(self) -> int:
         for c in self.contexts:
             c.__enter__()
-        return _stream()
+        return torch._C._cuda_getCurrentRawStream(self.dev)
 
     def __exit__(self, *exc):
-        for c in reversed(self.contexts):
+        for c in self.contexts:
             c.__exit__(*exc)
 
 
@@ -434,18 +443,18 @@ def quantize_act_token(x: torch.Tensor, stream=None):
     fp32 (see moe_quantize_act_token)."""
     ld = _matrix(x, _ROW_TYPES, "x")
     T, K = x.shape
-    with _On(x.device, stream) as s:
+    with _On(x.get_device(), stream) as s:
         q = torch.empty((T, K), dtype=torch.int8, device=x.device)
         d = torch.empty(T, dtype=torch.float32, device=x.device)
-        _check(lib().moe_quantize_act_token(_ptr(x), _DTYPES[x.dtype], T, K, ld, _ptr(q), K, _ptr(d), s),
-               "quantize_act_token")
+        _check(lib().moe_quantize_act_token(x.data_ptr(), _DTYPES[x.dtype], T, K, ld, q.data_ptr(), K, d.data_ptr(),
+                                            s), "quantize_act_token")
     return q, d
 
 
-def _result(out, T, N, dtype, device):
+def _result(out, T, N, dtype, like, dev):
     if out is None:
-        return torch.empty((T, N), dtype=dtype, device=device), N
-    return out, _matrix(out, (dtype,), "out", (T, N), device)
+        return torch.empty((T, N), dtype=dtype, device=like.device), N
+    return out, _matrix(out, (dtype,), "out", T, N, dev)
 
 
 def int8_matmul(xq: torch.Tensor, xd: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
@@ -454,19 +463,20 @@ def int8_matmul(xq: torch.Tensor, xd: torch.Tensor, w: torch.Tensor, s: torch.Te
     """(xq @ w.T) * xd[:, None] * s + bias: codes xq [T][K] with token scales xd
     [T], weight codes w [N][K] with row scales s [N] -> [T][N] of out_dtype.
     save=True also returns the int32 sums [T][N] that the backward pass reads."""
-    ldx, ldw = _matrix(xq, (torch.int8,), "xq"), _matrix(w, _CODE_TYPES, "w")
-    (T, K), N, dev = xq.shape, w.shape[0], xq.device
-    _matrix(w, _CODE_TYPES, "w", (N, K), dev)
+    ldx = _matrix(xq, _ACT_TYPES, "xq")
+    (T, K), dev = xq.shape, xq.get_device()
+    ldw = _matrix(w, _CODE_TYPES, "w", -1, K, dev)
+    N = w.shape[0]
     _vector(xd, T, "xd", dev)
     _vector(s, N, "s", dev)
     if bias is not None:
         _vector(bias, N, "bias", dev)
     dt = _choice(out_dtype, _DTYPES, "out_dtype")
     with _On(dev, stream) as st:
-        y, ldo = _result(out, T, N, out_dtype, dev)
-        acc = torch.empty((T, N), dtype=torch.int32, device=dev) if save else None
-        _check(lib().moe_int8_matmul(_ptr(xq), ldx, _ptr(xd), T, _ptr(w), ldw, _ptr(s), N, K, _ptr(bias), _ptr(y), dt,
-                                     ldo, _ptr(acc), st), "int8_matmul")
+        y, ldo = _result(out, T, N, out_dtype, xq, dev)
+        acc = torch.empty((T, N), dtype=torch.int32, device=xq.device) if save else None
+        _check(lib().moe_int8_matmul(xq.data_ptr(), ldx, xd.data_ptr(), T, w.data_ptr(), ldw, s.data_ptr(), N, K,
+                                     _addr(bias), y.data_ptr(), dt, ldo, _addr(acc), st), "int8_matmul")
     return (y, acc) if save else y
 
 
@@ -475,23 +485,26 @@ def int8_matmul_backward(dy: torch.Tensor, acc: torch.Tensor | None, xd: torch.T
     """Gradients of int8_matmul for dy [T][N]: dx [T][K] (of dy's type, with
     respect to the dequantised activations xd * xq), ds [N] and dbias [N] (fp32).
     acc=None leaves ds out (None), bias_grad=False dbias."""
-    lddy, ldw = _matrix(dy, _ROW_TYPES, "dy"), _matrix(w, _CODE_TYPES, "w", device=dy.device)
-    (T, N), K, dev = dy.shape, w.shape[1], dy.device
-    if w.shape[0] != N:
-        raise ValueError(f"w must have {N} rows, one for each column of dy, got {w.shape[0]}")
+    lddy = _matrix(dy, _ROW_TYPES, "dy")
+    (T, N), dev = dy.shape, dy.get_device()
+    ldw = _matrix(w, _CODE_TYPES, "w", N, -1, dev)
+    K = w.shape[1]
     _vector(s, N, "s", dev)
     if acc is not None:
         _sums(acc, (T, N), dev)
         _vector(xd, T, "xd", dev)
+    else:
+        xd = None
     dt = _DTYPES[dy.dtype]
     with _On(dev, stream) as st:
-        dx = torch.empty((T, K), dtype=dy.dtype, device=dev)
-        ds = torch.empty(N, dtype=torch.float32, device=dev) if acc is not None else None
-        db = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
-        ws = torch.empty(lib().moe_int8_backward_workspace_bytes(1, T, N, dt), dtype=torch.uint8, device=dev)
-        _check(lib().moe_int8_matmul_backward(_ptr(dy), dt, lddy, _ptr(acc), _ptr(xd if acc is not None else None), T,
-                                              _ptr(w), ldw, _ptr(s), N, K, _ptr(dx), K, _ptr(ds), _ptr(db), _ptr(ws),
-                                              ws.numel(), st), "int8_matmul_backward")
+        dx = torch.empty((T, K), dtype=dy.dtype, device=dy.device)
+        ds = torch.empty(N, dtype=torch.float32, device=dy.device) if acc is not None else None
+        db = torch.empty(N, dtype=torch.float32, device=dy.device) if bias_grad else None
+        size = lib().moe_int8_backward_workspace_bytes(1, T, N, dt)
+        ws = torch.empty(size, dtype=torch.uint8, device=dy.device)
+        _check(lib().moe_int8_matmul_backward(dy.data_ptr(), dt, lddy, _addr(acc), _addr(xd), T, w.data_ptr(), ldw,
+                                              s.data_ptr(), N, K, dx.data_ptr(), K, _addr(ds), _addr(db),
+                                              ws.data_ptr(), size, st), "int8_matmul_backward")
     return dx, ds, db
 
 
@@ -502,21 +515,21 @@ def gated_ffn(xq: torch.Tensor, xd: torch.Tensor, w_gate: torch.Tensor, s_gate: 
     [N][K], in one kernel; act is "silu" or "gelu" (tanh form) -> [T][N] of
     out_dtype.  save=True also returns the int32 sums [2][T][N] (gate, up) that
     the backward pass reads."""
-    ldx = _matrix(xq, (torch.int8,), "xq")
-    (T, K), dev = xq.shape, xq.device
-    ldg = _matrix(w_gate, _CODE_TYPES, "w_gate", device=dev)
+    ldx = _matrix(xq, _ACT_TYPES, "xq")
+    (T, K), dev = xq.shape, xq.get_device()
+    ldg = _matrix(w_gate, _CODE_TYPES, "w_gate", -1, K, dev)
     N = w_gate.shape[0]
-    _matrix(w_gate, _CODE_TYPES, "w_gate", (N, K), dev)
-    ldu = _matrix(w_up, _CODE_TYPES, "w_up", (N, K), dev)
+    ldu = _matrix(w_up, _CODE_TYPES, "w_up", N, K, dev)
     _vector(xd, T, "xd", dev)
     _vector(s_gate, N, "s_gate", dev)
     _vector(s_up, N, "s_up", dev)
     dt, ac = _choice(out_dtype, _DTYPES, "out_dtype"), _choice(act, _ACTS, "act")
     with _On(dev, stream) as st:
-        h, ldo = _result(out, T, N, out_dtype, dev)
-        acc = torch.empty((2, T, N), dtype=torch.int32, device=dev) if save else None
-        _check(lib().moe_gated_ffn(_ptr(xq), ldx, _ptr(xd), T, _ptr(w_gate), ldg, _ptr(s_gate), _ptr(w_up), ldu,
-                                   _ptr(s_up), N, K, ac, _ptr(h), dt, ldo, _ptr(acc), st), "gated_ffn")
+        h, ldo = _result(out, T, N, out_dtype, xq, dev)
+        acc = torch.empty((2, T, N), dtype=torch.int32, device=xq.device) if save else None
+        _check(lib().moe_gated_ffn(xq.data_ptr(), ldx, xd.data_ptr(), T, w_gate.data_ptr(), ldg, s_gate.data_ptr(),
+                                   w_up.data_ptr(), ldu, s_up.data_ptr(), N, K, ac, h.data_ptr(), dt, ldo, _addr(acc),
+                                   st), "gated_ffn")
     return (h, acc) if save else h
 
 
@@ -527,24 +540,25 @@ def gated_ffn_backward(dh: torch.Tensor, acc: torch.Tensor, xd: torch.Tensor, w_
     forward saved: dx [T][K] (of dh's type, with respect to the dequantised
     activations xd * xq), ds_gate [N] and ds_up [N] (fp32)."""
     lddh = _matrix(dh, _ROW_TYPES, "dh")
-    (T, N), dev = dh.shape, dh.device
-    ldg = _matrix(w_gate, _CODE_TYPES, "w_gate", device=dev)
+    (T, N), dev = dh.shape, dh.get_device()
+    ldg = _matrix(w_gate, _CODE_TYPES, "w_gate", N, -1, dev)
     K = w_gate.shape[1]
-    _matrix(w_gate, _CODE_TYPES, "w_gate", (N, K), dev)
-    ldu = _matrix(w_up, _CODE_TYPES, "w_up", (N, K), dev)
+    ldu = _matrix(w_up, _CODE_TYPES, "w_up", N, K, dev)
     _sums(acc, (2, T, N), dev)
     _vector(xd, T, "xd", dev)
     _vector(s_gate, N, "s_gate", dev)
     _vector(s_up, N, "s_up", dev)
     dt, ac = _DTYPES[dh.dtype], _choice(act, _ACTS, "act")
     with _On(dev, stream) as st:
-        dx = torch.empty((T, K), dtype=dh.dtype, device=dev)
-        dsg = torch.empty(N, dtype=torch.float32, device=dev)
-        dsu = torch.empty(N, dtype=torch.float32, device=dev)
-        ws = torch.empty(lib().moe_int8_backward_workspace_bytes(2, T, N, dt), dtype=torch.uint8, device=dev)
-        _check(lib().moe_gated_ffn_backward(_ptr(dh), dt, lddh, _ptr(acc), _ptr(xd), T, _ptr(w_gate), ldg,
-                                            _ptr(s_gate), _ptr(w_up), ldu, _ptr(s_up), N, K, ac, _ptr(dx), K,
-                                            _ptr(dsg), _ptr(dsu), _ptr(ws), ws.numel(), st), "gated_ffn_backward")
+        dx = torch.empty((T, K), dtype=dh.dtype, device=dh.device)
+        ds = torch.empty((2, N), dtype=torch.float32, device=dh.device)
+        size = lib().moe_int8_backward_workspace_bytes(2, T, N, dt)
+        ws = torch.empty(size, dtype=torch.uint8, device=dh.device)
+        dsg, dsu = ds.unbind()
+        _check(lib().moe_gated_ffn_backward(dh.data_ptr(), dt, lddh, acc.data_ptr(), xd.data_ptr(), T,
+                                            w_gate.data_ptr(), ldg, s_gate.data_ptr(), w_up.data_ptr(), ldu,
+                                            s_up.data_ptr(), N, K, ac, dx.data_ptr(), K, dsg.data_ptr(),
+                                            dsu.data_ptr(), ws.data_ptr(), size, st), "gated_ffn_backward")
     return dx, dsg, dsu
 
 
@@ -554,20 +568,23 @@ def dense_ffn(x: torch.Tensor, bank: ExpertBank, act: str = "silu", out: torch.T
     packed at wbits 8): matmul(quantise(gated(quantise(x)))), x [T][hidden] fp32,
     bf16 or fp16 -> the same shape and type."""
     ldx = _matrix(x, _ROW_TYPES, "x")
-    (T, H), dev = x.shape, x.device
+    (T, H), dev = x.shape, x.get_device()
     I = bank.w_gate.shape[1]
-    for name, t, shape in (("w_gate", bank.w_gate, (1, I, H)), ("w_up", bank.w_up, (1, I, H)),
-                           ("w_down", bank.w_down, (1, H, I)), ("s_gate", bank.s_gate, (1, I)),
-                           ("s_up", bank.s_up, (1, I)), ("s_down", bank.s_down, (1, H))):
-        want = torch.float32 if name[0] == "s" else torch.uint8
-        if t.dtype != want or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
-            raise ValueError(f"bank.{name} must be a contiguous {want} tensor {shape} on {dev} (one int8 expert)")
+    for name, t, shape, want in (("w_gate", bank.w_gate, (1, I, H), torch.uint8),
+                                 ("w_up", bank.w_up, (1, I, H), torch.uint8),
+                                 ("w_down", bank.w_down, (1, H, I), torch.uint8),
+                                 ("s_gate", bank.s_gate, (1, I), torch.float32),
+                                 ("s_up", bank.s_up, (1, I), torch.float32),
+                                 ("s_down", bank.s_down, (1, H), torch.float32)):
+        if t.dtype != want or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"bank.{name} must be a contiguous {want} tensor {shape} on cuda:{dev} (one int8 expert)")
     dt, ac = _DTYPES[x.dtype], _choice(act, _ACTS, "act")
     with _On(dev, stream) as st:
-        y, ldo = _result(out, T, H, x.dtype, dev)
-        ws = torch.empty(lib().moe_dense_ffn_workspace_bytes(T, H, I), dtype=torch.uint8, device=dev)
-        _check(lib().moe_dense_ffn(_ptr(x), dt, ldx, T, H, I, ctypes.byref(bank.struct()), ac, _ptr(y), ldo, _ptr(ws),
-                                   ws.numel(), st), "dense_ffn")
+        y, ldo = _result(out, T, H, x.dtype, x, dev)
+        size = lib().moe_dense_ffn_workspace_bytes(T, H, I)
+        ws = torch.empty(size, dtype=torch.uint8, device=x.device)
+        _check(lib().moe_dense_ffn(x.data_ptr(), dt, ldx, T, H, I, ctypes.byref(bank.struct()), ac, y.data_ptr(), ldo,
+                                   ws.data_ptr(), size, st), "dense_ffn")
     return y
 
 
