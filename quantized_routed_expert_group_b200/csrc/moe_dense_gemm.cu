@@ -507,6 +507,12 @@ constexpr int kPairCtl = 1024 + 4 * 2 * 256 * 8;  // barriers; each epilogue war
 constexpr int kPairSmem = kPairStages * 2 * kTileBytes + kPairCtl + 1024;
 constexpr int kPairRows = 256;
 
+// Tensor maps: a: the 256-row operand (grad: one a matrix), b: the column
+// operand (gated: one a CTA), small: the same in boxes for the parts of a tile.
+struct PairMaps {
+    CUtensorMap a[2], b[2], small[2];
+};
+
 struct PairParams {
     const float* xd;
     const float* s[kMaxMats];
@@ -520,7 +526,9 @@ struct PairParams {
     int k_steps, steps;
     int nt;            // matmul, grad: tokens of a tile; gated: channels of a tile
     int tiles_r;       // tiles along the 256 rows
-    int64_t tiles;
+    int64_t whole;     // tiles worked on whole
+    int parts;         // column parts of each tile after those
+    int64_t units;     // whole tiles and parts
     int act, dtype;
     int vec;           // gated: results and sums may be stored 16 bytes at a time
 };
@@ -586,6 +594,21 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uin
     }
 }
 
+// A unit of work: rows r0 .. r0 + 255, nt columns from c0.
+struct PairUnit {
+    int64_t r0, c0;
+    int nt;
+    bool part;
+};
+
+__device__ __forceinline__ PairUnit pair_unit(const PairParams& p, int64_t u) {
+    const bool part = u >= p.whole;
+    const int64_t tile = part ? p.whole + (u - p.whole) / p.parts : u;
+    const int nt = part ? p.nt / p.parts : p.nt;
+    const int64_t sub = part ? (u - p.whole) % p.parts : 0;
+    return PairUnit{tile % p.tiles_r * kPairRows, tile / p.tiles_r * p.nt + sub * nt, nt, part};
+}
+
 // Sixteen results of one token, channels n .. n + 15.
 __device__ __forceinline__ void store16(const PairParams& p, int64_t t, int n, const float (&v)[16]) {
     if (p.vec && n + 16 <= p.out_rows) {
@@ -630,8 +653,7 @@ __device__ __forceinline__ void store_acc16(const PairParams& p, int32_t* row, i
 
 template <int MODE, int P>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    k_dense_pair(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUtensorMap wmap1,
-                 const __grid_constant__ CUtensorMap xmap, const PairParams p) {
+    k_dense_pair(const __grid_constant__ PairMaps maps, const PairParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ctl = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(ctl);
@@ -646,7 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ncols = MODE == kGated ? 2 * p.nt : P * p.nt;  // the MMA's N
+    constexpr int kCols = MODE == kGated ? 2 : P;  // the MMA's columns for each of a unit's
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairStages; ++s) {
             mbar_init(&full[s], 1);
@@ -672,16 +694,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             // ---------------- producer (both CTAs) ----------------
-            tma_prefetch_map(&wmap0);
-            if (MODE != kMatmul) tma_prefetch_map(&wmap1);
-            tma_prefetch_map(&xmap);
+            const CUtensorMap* bw = &maps.b[MODE == kGated ? rank : 0];
+            const CUtensorMap* bs = &maps.small[MODE == kGated ? rank : 0];
+            tma_prefetch_map(&maps.a[0]);
+            if (MODE == kGrad) tma_prefetch_map(&maps.a[1]);
+            tma_prefetch_map(bw);
+            tma_prefetch_map(bs);
             int s = 0;
             uint32_t ph = 0;
             bool ok = true;
-            const uint32_t tx = 2 * (kTileBytes + ncols / 2 * kStageK);  // both CTAs' boxes
-            for (int64_t tile = pair; ok && tile < p.tiles; tile += pairs) {
-                const int r0 = (int)(tile % p.tiles_r) * kPairRows;
-                const int64_t c0 = tile / p.tiles_r * p.nt;
+            for (int64_t unit = pair; ok && unit < p.units; unit += pairs) {
+                const PairUnit u = pair_unit(p, unit);
+                const int r0 = (int)u.r0 + 128 * rank;
+                const CUtensorMap* bm = u.part ? bs : bw;
+                const uint32_t tx = 2 * (kTileBytes + kCols * u.nt / 2 * kStageK);  // both CTAs' boxes
                 for (int ks = 0; ks < p.steps; ++ks) {
                     if (!wait_cluster(&empty[s], ph ^ 1u, kWaitNs)) {
                         ok = false;
@@ -692,24 +718,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     uint8_t* st = sm + s * kStage;
                     if constexpr (MODE == kGrad) {
                         const int m = ks / p.k_steps, k = (ks - m * p.k_steps) * kStageK;
-                        tma_load_2d_pair(st, m ? &wmap1 : &wmap0, r0 + 128 * rank, k, bar);
+                        tma_load_2d_pair(st, &maps.a[m], r0, k, bar);
                         const int x = (int)(m * p.mat_pitch) + k;
                         if constexpr (P == 2) {  // one plane a CTA
-                            tma_load_2d_pair(st + kTileBytes, &xmap, x, (int)((int64_t)rank * p.T + c0), bar);
+                            tma_load_2d_pair(st + kTileBytes, bm, x, (int)((int64_t)rank * p.T + u.c0), bar);
                         } else {  // three halves of planes a CTA
 #pragma unroll
                             for (int j = 0; j < 3; ++j) {
                                 const int h = 3 * rank + j;
-                                tma_load_2d_pair(st + kTileBytes + j * p.nt / 2 * kStageK, &xmap, x,
-                                                 (int)((int64_t)(h >> 1) * p.T + c0 + (h & 1) * (p.nt / 2)), bar);
+                                tma_load_2d_pair(st + kTileBytes + j * (u.nt / 2) * kStageK, bm, x,
+                                                 (int)((int64_t)(h >> 1) * p.T + u.c0 + (h & 1) * (u.nt / 2)), bar);
                             }
                         }
-                    } else if constexpr (MODE == kMatmul) {
-                        tma_load_2d_pair(st, &wmap0, ks * kStageK, r0 + 128 * rank, bar);
-                        tma_load_2d_pair(st + kTileBytes, &xmap, ks * kStageK, (int)(c0 + rank * (p.nt / 2)), bar);
                     } else {
-                        tma_load_2d_pair(st, &xmap, ks * kStageK, r0 + 128 * rank, bar);
-                        tma_load_2d_pair(st + kTileBytes, rank ? &wmap1 : &wmap0, ks * kStageK, (int)c0, bar);
+                        tma_load_2d_pair(st, &maps.a[0], ks * kStageK, r0, bar);
+                        tma_load_2d_pair(st + kTileBytes, bm, ks * kStageK,
+                                         (int)(u.c0 + (MODE == kMatmul ? rank * (u.nt / 2) : 0)), bar);
                     }
                     if (++s == kPairStages) {
                         s = 0;
@@ -737,10 +761,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             int s = 0;
             uint32_t ph = 0;
             bool ok = true;
-            const uint32_t idesc = (idesc_tile<MODE>(ncols) & ~(31u << 24)) | ((uint32_t)(kPairRows >> 4) << 24);
             int nu = 0;
-            for (int64_t tile = pair; ok && tile < p.tiles; tile += pairs, ++nu) {
+            for (int64_t unit = pair; ok && unit < p.units; unit += pairs, ++nu) {
                 const int buf = nu & 1;
+                const uint32_t idesc = (idesc_tile<MODE>(kCols * pair_unit(p, unit).nt) & ~(31u << 24)) |
+                                       ((uint32_t)(kPairRows >> 4) << 24);
                 if (nu >= 2 && !wait_cluster(&acce[buf], ((nu >> 1) - 1) & 1, kWaitNs)) {
                     ok = false;
                     break;
@@ -776,12 +801,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // a copy for each warp: the epilogue warps never wait for one another
         RowScale* tok = reinterpret_cast<RowScale*>(ctl + 1024) + quad * 512;
         int nu = 0;
-        for (int64_t tile = pair; tile < p.tiles; tile += pairs, ++nu) {
+        for (int64_t unit = pair; unit < p.units; unit += pairs, ++nu) {
             const int buf = nu & 1;
-            const int64_t r0 = (tile % p.tiles_r) * kPairRows + 128 * rank;
-            const int64_t c0 = tile / p.tiles_r * p.nt;
+            const PairUnit un = pair_unit(p, unit);
+            const int64_t r0 = un.r0 + 128 * rank, c0 = un.c0;
+            const int nt = un.nt;
             RowScale* ts = tok + 256 * buf;
-            for (int i = lane; i < p.nt; i += 32) {
+            for (int i = lane; i < nt; i += 32) {
                 if constexpr (MODE == kGated)
                     ts[i] = c0 + i < p.rows ? RowScale{p.s[0][c0 + i], p.s[1][c0 + i]} : RowScale{0.0f, 0.0f};
                 else if (c0 + i < p.T)
@@ -805,10 +831,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 256 * buf;
             if constexpr (MODE == kGated) {
                 const int64_t t = r0 + row;
-                for (int c = 0; c < p.nt; c += 16) {
+                for (int c = 0; c < nt; c += 16) {
                     uint32_t g[16], u[16];
                     tmem_ld16(tl + c, g);
-                    tmem_ld16(tl + p.nt + c, u);
+                    tmem_ld16(tl + nt + c, u);
                     tmem_wait_ld();
                     if (t < p.T) {
                         float h[16];
@@ -826,11 +852,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
             } else {
                 const int64_t n = r0 + row;
-                const int nv = (int)min((int64_t)p.nt, p.T - c0);
+                const int nv = (int)min((int64_t)nt, p.T - c0);
                 for (int c = 0; c < nv; c += 16) {
                     uint32_t v[P][16];
 #pragma unroll
-                    for (int i = 0; i < P; ++i) tmem_ld16(tl + i * p.nt + c, v[i]);
+                    for (int i = 0; i < P; ++i) tmem_ld16(tl + i * nt + c, v[i]);
                     tmem_wait_ld();
                     if (n < p.out_rows) {
 #pragma unroll
@@ -999,24 +1025,54 @@ static cudaError_t run_pair(const GemmArgs& a, cudaStream_t s) {
             (!a.acc || (reinterpret_cast<uintptr_t>(a.acc) % 16 == 0 && a.rows % 4 == 0));
     p.nt = MODE == kGated ? 128 : MODE == kMatmul ? 256 : P == 2 ? 128 : 64;
     p.tiles_r = ((MODE == kGated ? a.T : p.out_rows) + kPairRows - 1) / kPairRows;
-    const int tiles_c = ((MODE == kGated ? a.rows : a.T) + p.nt - 1) / p.nt;
-    p.tiles = (int64_t)p.tiles_r * tiles_c;
-    // boxes of the three operands: the MMA's rows are 128 a CTA, its columns half of the pair's
-    const int wbox = MODE == kGated ? p.nt : 128;
-    const int xbox = MODE == kGated ? 128 : MODE == kMatmul ? p.nt / 2 : P == 2 ? p.nt : p.nt / 2;
-    CUtensorMap wm[kMaxMats], xm;
-    for (int m = 0; m < a.n_mats; ++m) {
-        e = encode_2d(&wm[m], a.w[m], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.cols, a.rows, a.ldw[m], kStageK, wbox,
-                      CU_TENSOR_MAP_SWIZZLE_128B);
-        if (e != cudaSuccess) return e;
-    }
-    if (a.n_mats == 1) wm[1] = wm[0];
-    e = encode_2d(&xm, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, MODE == kGrad ? a.n_mats * a.mat_pitch : a.cols,
-                  (uint64_t)a.planes * a.T, a.ldx, kStageK, xbox, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)p.tiles_r * (((MODE == kGated ? a.rows : a.T) + p.nt - 1) / p.nt);
+    // The tiles after the last full round of the pairs are cut into column
+    // parts where that ends sooner: a half costs 0.55 and a quarter 0.35 of a
+    // tile (the 256-row operand is loaded and read again for each part).
     const int64_t pairs = device_info().sm_count / 2;
-    const unsigned grid = 2 * (unsigned)(p.tiles < pairs ? p.tiles : pairs);
-    k_dense_pair<MODE, P><<<grid, kPairThreads, kPairSmem, s>>>(wm[0], wm[1], xm, p);
+    p.whole = tiles / pairs * pairs;
+    const int64_t rest = tiles - p.whole;
+    p.parts = 1;
+    double best = rest ? 1.0 : 0.0;
+    for (int q = 2; q <= (P == 3 ? 2 : 4); q *= 2) {
+        const double cost = (double)((rest * q + pairs - 1) / pairs) * (q == 2 ? 0.55 : 0.35);
+        if (cost < best) {
+            best = cost;
+            p.parts = q;
+        }
+    }
+    p.units = p.whole + rest * p.parts;
+    // boxes: the MMA's rows are 128 a CTA, its columns half of the pair's
+    PairMaps maps;
+    auto map_w = [&](CUtensorMap* m, int i, int box) {
+        return encode_2d(m, a.w[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.cols, a.rows, a.ldw[i], kStageK, box,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    auto map_x = [&](CUtensorMap* m, int box) {
+        return encode_2d(m, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, MODE == kGrad ? a.n_mats * a.mat_pitch : a.cols,
+                         (uint64_t)a.planes * a.T, a.ldx, kStageK, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    const int half = MODE == kGrad && P == 2 ? p.nt : MODE == kGated ? p.nt : p.nt / 2;
+    if constexpr (MODE == kGated) {
+        e = map_x(&maps.a[0], 128);
+        for (int m = 0; m < 2 && e == cudaSuccess; ++m) {
+            e = map_w(&maps.b[m], m, half);
+            if (e == cudaSuccess && p.parts > 1) e = map_w(&maps.small[m], m, half / p.parts);
+        }
+    } else {
+        for (int m = 0; m < a.n_mats && e == cudaSuccess; ++m) e = map_w(&maps.a[m], m, 128);
+        if (e == cudaSuccess) e = map_x(&maps.b[0], half);
+        if (e == cudaSuccess && p.parts > 1) e = map_x(&maps.small[0], half / p.parts);
+    }
+    if (e != cudaSuccess) return e;
+    if (MODE != kGrad || a.n_mats == 1) maps.a[1] = maps.a[0];
+    if (MODE != kGated) maps.b[1] = maps.b[0];
+    if (p.parts == 1)
+        for (int m = 0; m < 2; ++m) maps.small[m] = maps.b[m];
+    else if (MODE != kGated)
+        maps.small[1] = maps.small[0];
+    const unsigned grid = 2 * (unsigned)(p.units < pairs ? p.units : pairs);
+    k_dense_pair<MODE, P><<<grid, kPairThreads, kPairSmem, s>>>(maps, p);
     return cudaGetLastError();
 }
 
