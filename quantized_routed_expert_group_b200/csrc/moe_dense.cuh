@@ -11,6 +11,7 @@
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,6 +45,16 @@ struct Elem<MOE_F16> {
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+template <typename OT>
+__device__ __forceinline__ OT from_f32(float v) {
+    if constexpr (sizeof(OT) == 4)
+        return v;
+    else if constexpr (std::is_same<OT, __nv_bfloat16>::value)
+        return __float2bfloat16_rn(v);
+    else
+        return __float2half_rn(v);
+}
 
 // One result element, rounded once to its type.
 __device__ __forceinline__ void store_elem(void* out, int64_t i, int dtype, float v) {

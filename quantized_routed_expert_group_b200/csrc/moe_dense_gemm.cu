@@ -126,26 +126,68 @@ __device__ __forceinline__ int ld_peer(const int32_t* p, uint32_t rank) {
     return v;
 }
 
-// Joins a token's sums of one channel and stores the result.
-template <int MODE, int P>
-__device__ __forceinline__ void finish(const TileParams& p, const int (&v)[MODE == kGated ? 2 : P], int64_t t, int n,
-                                       float ta, float tb, float s0, float s1, float bias) {
-    if constexpr (MODE == kGrad) {
-        // digits joined in fp32: each plane's sum rounds by 2^-24 of itself
-        float f = (float)v[P - 1];
+// Where a product's results go, for lanes that are channels.
+struct ChannelOut {
+    void* out;
+    int64_t ldo;
+    int32_t* acc;
+    int64_t acc_pitch;  // gated: from the gate's sums to the up projection's
+    int rows;           // row length of acc
+    int act;
+};
+
+// The results of one channel n for up to N consecutive tokens t ..: `v` are the
+// integer sums (gated: gate and up; gradient: planes), `ts` the tokens' scales
+// (16-byte aligned).  All values are formed before the first store, so that the
+// columns' arithmetic overlaps; a warp's stores run along the tokens' rows.
+template <int MODE, int P, typename OT, int N>
+__device__ __forceinline__ void emit_channel(const ChannelOut& o, const uint32_t (&v)[MODE == kGated ? 2 : P][N],
+                                             int64_t t, int n, int valid, const RowScale* ts, float s0, float s1,
+                                             float bias) {
+    float f[N];
 #pragma unroll
-        for (int i = P - 2; i >= 0; --i) f = fmaf(f, 256.0f, (float)v[i]);
-        store_elem(p.out, t * p.ldo + n, p.dtype, f * ta * tb);
-    } else {
-        if (p.acc) {
-            p.acc[t * p.rows + n] = v[0];
-            if constexpr (MODE == kGated) p.acc[((int64_t)p.T + t) * p.rows + n] = v[1];
+    for (int j = 0; j < N; j += 2) {
+        const float4 sc = *reinterpret_cast<const float4*>(ts + j);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float a = k ? sc.z : sc.x, b = k ? sc.w : sc.y;
+            if constexpr (MODE == kGrad) {
+                // digits joined in fp32: each plane's sum rounds by 2^-24 of itself
+                float d = (float)(int)v[P - 1][j + k];
+#pragma unroll
+                for (int i = P - 2; i >= 0; --i) d = fmaf(d, 256.0f, (float)(int)v[i][j + k]);
+                f[j + k] = d * a * b;
+            } else if constexpr (MODE == kGated) {
+                f[j + k] = act_value(o.act, (float)(int)v[0][j + k] * (a * s0)) * ((float)(int)v[1][j + k] * (a * s1));
+            } else {
+                f[j + k] = (float)(int)v[0][j + k] * (a * s0) + bias;
+            }
         }
-        const float y = (float)v[0] * (ta * s0);
-        if constexpr (MODE == kGated)
-            store_elem(p.out, t * p.ldo + n, p.dtype, act_value(p.act, y) * ((float)v[1] * (ta * s1)));
-        else
-            store_elem(p.out, t * p.ldo + n, p.dtype, y + bias);
+    }
+    OT* out = static_cast<OT*>(o.out) + t * o.ldo + n;
+    if (valid >= N) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            *out = from_f32<OT>(f[j]);
+            out += o.ldo;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (j < valid) *out = from_f32<OT>(f[j]);
+            out += o.ldo;
+        }
+    }
+    if (MODE != kGrad && o.acc) {
+#pragma unroll
+        for (int m = 0; m < (MODE == kGated ? 2 : 1); ++m) {
+            int32_t* acc = o.acc + m * o.acc_pitch + t * o.rows + n;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (j < valid) *acc = (int)v[m][j];
+                acc += o.rows;
+            }
+        }
     }
 }
 
@@ -153,7 +195,7 @@ __device__ __forceinline__ void finish(const TileParams& p, const int (&v)[MODE 
 // contraction and add their integer sums through distributed shared memory
 // (exact, so the split changes no bit).  Every wait is bounded by the global
 // timer and records kErrTimeout.
-template <int MODE, int P>
+template <int MODE, int P, typename OT>
 __global__ void __launch_bounds__(kTileThreads)
     k_dense_tile(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUtensorMap wmap1,
                  const __grid_constant__ CUtensorMap xmap, const TileParams p) {
@@ -192,8 +234,8 @@ __global__ void __launch_bounds__(kTileThreads)
         tmem_alloc(tmem_slot, p.tmem_cols);
         tmem_relinquish();
     }
-    for (int i = threadIdx.x; i < nv; i += kTileThreads)
-        tok[i] = MODE == kGrad ? p.gscale[t0 + i] : RowScale{p.xd[t0 + i], 1.0f};
+    for (int i = threadIdx.x; i < p.nt; i += kTileThreads)
+        tok[i] = i >= nv ? RowScale{0.0f, 0.0f} : MODE == kGrad ? p.gscale[t0 + i] : RowScale{p.xd[t0 + i], 1.0f};
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -313,6 +355,7 @@ __global__ void __launch_bounds__(kTileThreads)
     const int n = n0 + ch;
     float s0 = 0.0f, s1 = 0.0f, bias = 0.0f;
     int32_t* part = reinterpret_cast<int32_t*>(sm);  // split: [column][128] sums of this CTA
+    const ChannelOut co{p.out, p.ldo, p.acc, (int64_t)p.T * p.rows, p.rows, p.act};
     if (warp >= 2) {
         if constexpr (MODE != kGrad) {
             if (n < p.out_rows) {
@@ -329,17 +372,13 @@ __global__ void __launch_bounds__(kTileThreads)
 #pragma unroll
             for (int i = 0; i < kV; ++i) tmem_ld16(tl + i * p.nt + c, r[i]);
             tmem_wait_ld();
+            if (split > 1) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                if (split > 1) {
+                for (int j = 0; j < 16; ++j)
 #pragma unroll
                     for (int i = 0; i < kV; ++i) part[(i * p.nt + c + j) * 128 + ch] = (int)r[i][j];
-                } else if (c + j < nv && n < p.out_rows) {
-                    int v[kV];
-#pragma unroll
-                    for (int i = 0; i < kV; ++i) v[i] = (int)r[i][j];
-                    finish<MODE, P>(p, v, t0 + c + j, n, tok[c + j].a, tok[c + j].b, s0, s1, bias);
-                }
+            } else if (n < p.out_rows) {
+                emit_channel<MODE, P, OT, 16>(co, r, t0 + c, n, nv - c, tok + c, s0, s1, bias);
             }
         }
     }
@@ -352,16 +391,18 @@ __global__ void __launch_bounds__(kTileThreads)
     if (split > 1) {
         cluster_sync_all();
         if (warp >= 2 && n < p.out_rows) {
-            const int per = (nv + (int)split - 1) / (int)split;
-            const int c1 = min(nv, (int)(rank + 1) * per);
-            for (int c = (int)rank * per; c < c1; ++c) {
-                int v[kV];
+            // the tokens are dealt to the CTAs in pairs
+            for (int c = 2 * (int)rank; c < nv; c += 2 * (int)split) {
+                uint32_t v[kV][2];
 #pragma unroll
-                for (int i = 0; i < kV; ++i) v[i] = 0;
+                for (int i = 0; i < kV; ++i) v[i][0] = v[i][1] = 0;
                 for (uint32_t q = 0; q < split; ++q)
 #pragma unroll
-                    for (int i = 0; i < kV; ++i) v[i] += ld_peer(&part[(i * p.nt + c) * 128 + ch], q);
-                finish<MODE, P>(p, v, t0 + c, n, tok[c].a, tok[c].b, s0, s1, bias);
+                    for (int i = 0; i < kV; ++i) {
+                        v[i][0] += ld_peer(&part[(i * p.nt + c) * 128 + ch], q);
+                        v[i][1] += ld_peer(&part[(i * p.nt + c + 1) * 128 + ch], q);
+                    }
+                emit_channel<MODE, P, OT, 2>(co, v, t0 + c, n, nv - c, tok + c, s0, s1, bias);
             }
         }
         cluster_sync_all();  // the peers have read this CTA's sums
@@ -501,9 +542,9 @@ __global__ void __launch_bounds__(kDotThreads) k_dense_dot(const DotParams p) {
 //     is a channel, and a warp's stores run along a token's row
 //   gated: rows = 256 tokens, columns = 128 gate and 128 up channels (one half
 //     from each CTA), so that a lane holds a token's g and u of one channel
-constexpr int kPairThreads = 192;
+constexpr int kPairThreads = 320;  // producer warp, MMA warp, eight epilogue warps
 constexpr int kPairStages = 6;
-constexpr int kPairCtl = 1024 + 4 * 2 * 256 * 8;  // barriers; each epilogue warp's scales of two tiles' columns
+constexpr int kPairCtl = 1024 + 8 * 2 * 128 * 8;  // barriers; each epilogue warp's scales of two tiles' columns
 constexpr int kPairSmem = kPairStages * 2 * kTileBytes + kPairCtl + 1024;
 constexpr int kPairRows = 256;
 
@@ -610,32 +651,20 @@ __device__ __forceinline__ PairUnit pair_unit(const PairParams& p, int64_t u) {
 }
 
 // Sixteen results of one token, channels n .. n + 15.
+template <typename OT>
 __device__ __forceinline__ void store16(const PairParams& p, int64_t t, int n, const float (&v)[16]) {
+    OT* o = static_cast<OT*>(p.out) + t * p.ldo + n;
+    alignas(16) OT e[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) e[i] = from_f32<OT>(v[i]);
     if (p.vec && n + 16 <= p.out_rows) {
-        if (p.dtype == MOE_F32) {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + t * p.ldo + n);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (p.dtype == MOE_BF16) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                } else {
-                    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-            }
-            uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + t * p.ldo + n);
-            o[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            o[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        }
+        for (int i = 0; i < (int)sizeof(e) / 16; ++i)
+            reinterpret_cast<uint4*>(o)[i] = reinterpret_cast<const uint4*>(e)[i];
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (n + i < p.out_rows) store_elem(p.out, t * p.ldo + n + i, p.dtype, v[i]);
+            if (n + i < p.out_rows) o[i] = e[i];
     }
 }
 
@@ -651,7 +680,7 @@ __device__ __forceinline__ void store_acc16(const PairParams& p, int32_t* row, i
     }
 }
 
-template <int MODE, int P>
+template <int MODE, int P, typename OT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_dense_pair(const __grid_constant__ PairMaps maps, const PairParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -676,7 +705,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accf[b], 1);
-            mbar_init(&acce[b], 8);  // four epilogue warps of each CTA
+            mbar_init(&acce[b], 16);  // the epilogue warps of both CTAs
         }
         fence_barrier_init();
     }
@@ -796,87 +825,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---------------- epilogue: warps 2..5 = TMEM lane quarters 2, 3, 0, 1 ----------------
-        const int quad = warp & 3, row = 32 * quad + lane;
+        // ---------------- epilogue: two warps a TMEM lane quarter, half of the columns each ----------------
+        const int quad = warp & 3, row = 32 * quad + lane, half = (warp - 2) >> 2;
         // a copy for each warp: the epilogue warps never wait for one another
-        RowScale* tok = reinterpret_cast<RowScale*>(ctl + 1024) + quad * 512;
+        RowScale* tok = reinterpret_cast<RowScale*>(ctl + 1024) + (warp - 2) * 256;
+        const ChannelOut co{p.out, p.ldo, p.acc, (int64_t)p.T * p.rows, p.rows, p.act};
         int nu = 0;
         for (int64_t unit = pair; unit < p.units; unit += pairs, ++nu) {
             const int buf = nu & 1;
             const PairUnit un = pair_unit(p, unit);
-            const int64_t r0 = un.r0 + 128 * rank, c0 = un.c0;
-            const int nt = un.nt;
-            RowScale* ts = tok + 256 * buf;
-            for (int i = lane; i < nt; i += 32) {
-                if constexpr (MODE == kGated)
-                    ts[i] = c0 + i < p.rows ? RowScale{p.s[0][c0 + i], p.s[1][c0 + i]} : RowScale{0.0f, 0.0f};
-                else if (c0 + i < p.T)
-                    ts[i] = MODE == kGrad ? p.gscale[c0 + i] : RowScale{p.xd[c0 + i], 1.0f};
+            const int cols = un.nt / 2;  // this warp's columns: cols from c0 on
+            const int64_t r0 = un.r0 + 128 * rank + row, c0 = un.c0 + half * cols;
+            RowScale* ts = tok + 128 * buf;
+            for (int i = lane; i < cols; i += 32) {
+                RowScale sc{0.0f, 0.0f};
+                if constexpr (MODE == kGated) {
+                    if (c0 + i < p.rows) sc = RowScale{p.s[0][c0 + i], p.s[1][c0 + i]};
+                } else {
+                    if (c0 + i < p.T) sc = MODE == kGrad ? p.gscale[c0 + i] : RowScale{p.xd[c0 + i], 1.0f};
+                }
+                ts[i] = sc;
             }
             float sa = 0.0f, bias = 0.0f;
             if constexpr (MODE == kGated) {
-                if (r0 + row < p.T) sa = p.xd[r0 + row];
+                if (r0 < p.T) sa = p.xd[r0];
             } else if constexpr (MODE == kMatmul) {
-                if (r0 + row < p.out_rows) {
-                    sa = p.s[0][r0 + row];
-                    if (p.bias) bias = p.bias[r0 + row];
+                if (r0 < p.out_rows) {
+                    sa = p.s[0][r0];
+                    if (p.bias) bias = p.bias[r0];
                 }
             }
+            __syncwarp();
             // (a whole warp gives up together)
             if (!__all_sync(kFull, wait_cluster(&accf[buf], (uint32_t)(nu >> 1) & 1u, kWaitAllNs))) {
                 set_error(&g_dense_error, kErrTimeout);
                 break;
             }
             tc_fence_after_sync();
-            const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 256 * buf;
+            const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 256 * buf + half * cols;
             if constexpr (MODE == kGated) {
-                const int64_t t = r0 + row;
-                for (int c = 0; c < nt; c += 16) {
+                for (int c = 0; c < cols; c += 16) {
                     uint32_t g[16], u[16];
                     tmem_ld16(tl + c, g);
-                    tmem_ld16(tl + nt + c, u);
+                    tmem_ld16(tl + un.nt + c, u);
                     tmem_wait_ld();
-                    if (t < p.T) {
+                    if (r0 < p.T) {
                         float h[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const RowScale sc = ts[c + j];
                             h[j] = act_value(p.act, (float)(int)g[j] * (sa * sc.a)) * ((float)(int)u[j] * (sa * sc.b));
                         }
-                        store16(p, t, (int)c0 + c, h);
+                        store16<OT>(p, r0, (int)c0 + c, h);
                         if (p.acc) {
-                            store_acc16(p, p.acc + t * p.rows, (int)c0 + c, g);
-                            store_acc16(p, p.acc + (p.T + t) * p.rows, (int)c0 + c, u);
+                            store_acc16(p, p.acc + r0 * p.rows, (int)c0 + c, g);
+                            store_acc16(p, p.acc + (p.T + r0) * p.rows, (int)c0 + c, u);
                         }
                     }
                 }
             } else {
-                const int64_t n = r0 + row;
-                const int nv = (int)min((int64_t)nt, p.T - c0);
+                const int nv = (int)min((int64_t)cols, p.T - c0);
                 for (int c = 0; c < nv; c += 16) {
                     uint32_t v[P][16];
 #pragma unroll
-                    for (int i = 0; i < P; ++i) tmem_ld16(tl + i * nt + c, v[i]);
+                    for (int i = 0; i < P; ++i) tmem_ld16(tl + i * un.nt + c, v[i]);
                     tmem_wait_ld();
-                    if (n < p.out_rows) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (c + j >= nv) break;
-                            const RowScale sc = ts[c + j];
-                            const int64_t t = c0 + c + j;
-                            float f;
-                            if constexpr (MODE == kGrad) {
-                                f = (float)(int)v[P - 1][j];
-#pragma unroll
-                                for (int i = P - 2; i >= 0; --i) f = fmaf(f, 256.0f, (float)(int)v[i][j]);
-                                f = f * sc.a * sc.b;
-                            } else {
-                                if (p.acc) p.acc[t * p.rows + n] = (int)v[0][j];
-                                f = (float)(int)v[0][j] * (sc.a * sa) + bias;
-                            }
-                            store_elem(p.out, t * p.ldo + n, p.dtype, f);
-                        }
-                    }
+                    if (r0 < p.out_rows)
+                        emit_channel<MODE, P, OT, 16>(co, v, c0 + c, (int)r0, nv - c, ts + c, sa, 0.0f, bias);
                 }
             }
             tc_fence_before_sync();
@@ -910,10 +925,10 @@ static cudaError_t allow_smem(K kernel, bool (&done)[64]) {
     return e;
 }
 
-template <int MODE, int P>
+template <int MODE, int P, typename OT>
 static cudaError_t run_tile(const GemmArgs& a, cudaStream_t s) {
     static bool attr_done[64];
-    cudaError_t e = allow_smem(k_dense_tile<MODE, P>, attr_done);
+    cudaError_t e = allow_smem(k_dense_tile<MODE, P, OT>, attr_done);
     if (e != cudaSuccess) return e;
     constexpr int kA = MODE == kGated ? 2 : 1;
     TileParams p{};
@@ -995,13 +1010,13 @@ static cudaError_t run_tile(const GemmArgs& a, cudaStream_t s) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_dense_tile<MODE, P>, wm[0], wm[1], xm, p);
+    return cudaLaunchKernelEx(&cfg, k_dense_tile<MODE, P, OT>, wm[0], wm[1], xm, p);
 }
 
-template <int MODE, int P>
+template <int MODE, int P, typename OT>
 static cudaError_t run_pair(const GemmArgs& a, cudaStream_t s) {
     static bool attr_done[64];
-    cudaError_t e = allow_smem(k_dense_pair<MODE, P>, attr_done);
+    cudaError_t e = allow_smem(k_dense_pair<MODE, P, OT>, attr_done);
     if (e != cudaSuccess) return e;
     PairParams p{};
     p.xd = a.xd;
@@ -1072,7 +1087,7 @@ static cudaError_t run_pair(const GemmArgs& a, cudaStream_t s) {
     else if (MODE != kGated)
         maps.small[1] = maps.small[0];
     const unsigned grid = 2 * (unsigned)(p.units < pairs ? p.units : pairs);
-    k_dense_pair<MODE, P><<<grid, kPairThreads, kPairSmem, s>>>(maps, p);
+    k_dense_pair<MODE, P, OT><<<grid, kPairThreads, kPairSmem, s>>>(maps, p);
     return cudaGetLastError();
 }
 
@@ -1133,22 +1148,27 @@ static cudaError_t run_dot(const GemmArgs& a, cudaStream_t s) {
 constexpr int kDotTokens = 4;
 constexpr int kPairTokens = 256;
 
-cudaError_t launch_matmul(const GemmArgs& a, cudaStream_t s) {
-    if (a.T <= kDotTokens) return run_dot<kMatmul>(a, s);
-    if (a.T >= kPairTokens && tma_operands(a)) return run_pair<kMatmul, 1>(a, s);
-    return run_tile<kMatmul, 1>(a, s);
+template <int MODE, int P, typename OT>
+static cudaError_t run_product(const GemmArgs& a, cudaStream_t s) {
+    return a.T >= kPairTokens && tma_operands(a) ? run_pair<MODE, P, OT>(a, s) : run_tile<MODE, P, OT>(a, s);
 }
 
-cudaError_t launch_gated(const GemmArgs& a, cudaStream_t s) {
-    if (a.T <= kDotTokens) return run_dot<kGated>(a, s);
-    if (a.T >= kPairTokens && tma_operands(a)) return run_pair<kGated, 1>(a, s);
-    return run_tile<kGated, 1>(a, s);
+template <int MODE>
+static cudaError_t run_forward(const GemmArgs& a, cudaStream_t s) {
+    if (a.T <= kDotTokens) return run_dot<MODE>(a, s);
+    return a.dtype == MOE_F32    ? run_product<MODE, 1, float>(a, s)
+           : a.dtype == MOE_BF16 ? run_product<MODE, 1, __nv_bfloat16>(a, s)
+                                 : run_product<MODE, 1, __half>(a, s);
 }
+
+cudaError_t launch_matmul(const GemmArgs& a, cudaStream_t s) { return run_forward<kMatmul>(a, s); }
+
+cudaError_t launch_gated(const GemmArgs& a, cudaStream_t s) { return run_forward<kGated>(a, s); }
 
 cudaError_t launch_grad_matmul(const GemmArgs& a, cudaStream_t s) {
-    if (a.T >= kPairTokens && tma_operands(a))
-        return a.planes == 2 ? run_pair<kGrad, 2>(a, s) : run_pair<kGrad, 3>(a, s);
-    return a.planes == 2 ? run_tile<kGrad, 2>(a, s) : run_tile<kGrad, 3>(a, s);
+    return a.dtype == MOE_F32    ? run_product<kGrad, planes_of(MOE_F32), float>(a, s)
+           : a.dtype == MOE_BF16 ? run_product<kGrad, planes_of(MOE_BF16), __nv_bfloat16>(a, s)
+                                 : run_product<kGrad, planes_of(MOE_F16), __half>(a, s);
 }
 
 cudaError_t read_device_error(cudaStream_t s, int32_t* code) {
