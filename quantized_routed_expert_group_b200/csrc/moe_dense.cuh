@@ -78,7 +78,7 @@ constexpr float kGelu1 = 0.044715f;
 __device__ __forceinline__ float act_value(int act, float g) {
     const float z = act == MOE_ACT_SILU ? g : kGelu0 * (g + kGelu1 * g * g * g);
     const float e = expf(-fabsf(z));
-    const float r = __fdiv_rn(1.0f, 1.0f + e);
+    const float r = __frcp_rn(1.0f + e);
     return g * (z >= 0.0f ? r : e * r);
 }
 
@@ -86,7 +86,7 @@ __device__ __forceinline__ void act_value_grad(int act, float g, float& a, float
     const float z = act == MOE_ACT_SILU ? g : kGelu0 * (g + kGelu1 * g * g * g);
     const float dz = act == MOE_ACT_SILU ? 1.0f : kGelu0 * (1.0f + 3.0f * kGelu1 * g * g);
     const float e = expf(-fabsf(z));
-    const float r = __fdiv_rn(1.0f, 1.0f + e);
+    const float r = __frcp_rn(1.0f + e);
     const float sig = z >= 0.0f ? r : e * r;
     const float dsig = e * r * r;
     a = g * sig;
@@ -96,8 +96,9 @@ __device__ __forceinline__ void act_value_grad(int act, float g, float& a, float
 
 // ---------------------------------------------------------------------------
 // Fixed-point planes of a gradient row.  A row v with m = max|v| is written as
-// the integers round(v D / m), D = 127 (256^P - 1) / 255 of P signed base-256
-// digits with the top one in [-127, 127], so that
+// the integers round(v D / m) of P signed base-256 digits, D = 32639 for P = 2
+// (127 in both digits) and 8355600 for P = 3 (some hundred below 127 in all
+// three, so that the product's rounding never lifts the top digit), so that
 //   sum_n v_n w_n = (m / D) sum_p 256^p (digit_p . w)
 // runs as P int8 products against the packed weight rows as they lie, each
 // exact in int32.  The only rounding is the one to the row's fixed point: at
@@ -107,7 +108,7 @@ __device__ __forceinline__ void act_value_grad(int act, float g, float& a, float
 // ---------------------------------------------------------------------------
 constexpr int planes_of(int dtype) { return dtype == MOE_F32 ? 3 : 2; }
 template <int P>
-constexpr float kPlaneMax = P == 2 ? 32639.0f : 8355711.0f;
+constexpr float kPlaneMax = P == 2 ? 32639.0f : 8355600.0f;
 
 // A row scale: value = integer * a * b (b a power of two that keeps a normal
 // when the row is tiny).

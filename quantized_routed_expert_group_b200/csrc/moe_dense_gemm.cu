@@ -543,9 +543,13 @@ __global__ void __launch_bounds__(kDotThreads) k_dense_dot(const DotParams p) {
 //   gated: rows = 256 tokens, columns = 128 gate and 128 up channels (one half
 //     from each CTA), so that a lane holds a token's g and u of one channel
 constexpr int kPairThreads = 320;  // producer warp, MMA warp, eight epilogue warps
-constexpr int kPairStages = 6;
+// (the gated kernel gives a stage's room to its epilogue's staging)
+template <int MODE>
+constexpr int kPairStages = MODE == kGated ? 5 : 6;
+constexpr int kStageWarp = 32 * 144;  // a warp's staging: 32 rows of 128 bytes, padded
 constexpr int kPairCtl = 1024 + 8 * 2 * 128 * 8;  // barriers; each epilogue warp's scales of two tiles' columns
-constexpr int kPairSmem = kPairStages * 2 * kTileBytes + kPairCtl + 1024;
+template <int MODE>
+constexpr int kPairSmem = kPairStages<MODE> * 2 * kTileBytes + kPairCtl + 1024 + (MODE == kGated ? 8 * kStageWarp : 0);
 constexpr int kPairRows = 256;
 
 // Tensor maps: a: the 256-row operand (grad: one a matrix), b: the column
@@ -680,14 +684,51 @@ __device__ __forceinline__ void store_acc16(const PairParams& p, int32_t* row, i
     }
 }
 
+// 32 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// 32 values of each of a warp's 32 rows (a lane holds its row's columns n ..
+// n + 31) to rows t0 .. of [T][N] at n, through the warp's staging buffer: a row
+// is written by 32 * sizeof(V) / 16 neighbouring lanes.  N and ld are multiples of 16 bytes.
+template <typename V, typename W>
+__device__ __forceinline__ void store_rows32(V* out, int64_t ld, int64_t T, int N, int64_t t0, int n,
+                                             const W (&v)[32], uint8_t* stage, int lane) {
+    static_assert(sizeof(V) == sizeof(W), "the same elements");
+    constexpr int kPieces = 32 * (int)sizeof(V) / 16, kPitch = 16 * kPieces + 16, kEach = 16 / (int)sizeof(V);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+        *reinterpret_cast<uint4*>(stage + lane * kPitch + 16 * i) = reinterpret_cast<const uint4*>(v)[i];
+    __syncwarp();
+    const int piece = lane % kPieces;
+    const bool in = n + (piece + 1) * kEach <= N;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        const int row = i * (32 / kPieces) + lane / kPieces;
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + row * kPitch + 16 * piece);
+        if (in && t0 + row < T) *reinterpret_cast<uint4*>(out + (t0 + row) * ld + n + piece * kEach) = w;
+    }
+    __syncwarp();
+}
+
 template <int MODE, int P, typename OT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_dense_pair(const __grid_constant__ PairMaps maps, const PairParams p) {
+    constexpr int kStages = kPairStages<MODE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ctl = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(ctl);
-    uint64_t* empty = full + kPairStages;
-    uint64_t* accf = empty + kPairStages;  // [2]
+    uint64_t* empty = full + kStages;
+    uint64_t* accf = empty + kStages;  // [2]
     uint64_t* acce = accf + 2;             // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
     uint8_t* sm = ctl + kPairCtl;
@@ -699,7 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kCols = MODE == kGated ? 2 : P;  // the MMA's columns for each of a unit's
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPairStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -764,7 +805,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         tma_load_2d_pair(st + kTileBytes, bm, ks * kStageK,
                                          (int)(u.c0 + (MODE == kMatmul ? rank * (u.nt / 2) : 0)), bar);
                     }
-                    if (++s == kPairStages) {
+                    if (++s == kStages) {
                         s = 0;
                         ph ^= 1u;
                     }
@@ -772,12 +813,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
             if (!ok) set_error(&g_dense_error, kErrTimeout);
             // every box has been consumed before the CTA ends
-            for (int i = 0; i < kPairStages; ++i) {
+            for (int i = 0; i < kStages; ++i) {
                 if (!wait_cluster(&empty[s], ph ^ 1u, kWaitNs)) {
                     set_error(&g_dense_error, kErrTimeout);
                     break;
                 }
-                if (++s == kPairStages) {
+                if (++s == kStages) {
                     s = 0;
                     ph ^= 1u;
                 }
@@ -814,7 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     for (int j = 0; j < kStageK / 32; ++j)
                         mma_i8_pair(d, a0 + (MODE == kGrad ? 256 * j : 2 * j), b0 + 2 * j, idesc, ks > 0 || j > 0);
                     mma_commit_pair(&empty[s]);
-                    if (++s == kPairStages) {
+                    if (++s == kStages) {
                         s = 0;
                         ph ^= 1u;
                     }
@@ -864,7 +905,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tc_fence_after_sync();
             const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 256 * buf + half * cols;
             if constexpr (MODE == kGated) {
-                for (int c = 0; c < cols; c += 16) {
+                int c = 0;
+                if (p.vec) {
+                    // 32 channels at a time, turned in shared memory so that the
+                    // stores run along the tokens' rows
+                    uint8_t* stage = sm + kStages * kStage + (warp - 2) * kStageWarp;
+                    const int64_t t0 = r0 - lane;
+                    for (; c + 32 <= cols; c += 32) {
+                        uint32_t g[32], u[32];
+                        tmem_ld32(tl + c, g);
+                        tmem_ld32(tl + un.nt + c, u);
+                        tmem_wait_ld();
+                        if (p.acc) {
+                            store_rows32(p.acc, p.rows, p.T, p.rows, t0, (int)c0 + c, g, stage, lane);
+                            store_rows32(p.acc + p.T * (int64_t)p.rows, p.rows, p.T, p.rows, t0, (int)c0 + c, u,
+                                         stage, lane);
+                        }
+                        alignas(16) OT h[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const RowScale sc = ts[c + j];
+                            h[j] = from_f32<OT>(act_value(p.act, (float)(int)g[j] * (sa * sc.a)) *
+                                                ((float)(int)u[j] * (sa * sc.b)));
+                        }
+                        store_rows32(static_cast<OT*>(p.out), p.ldo, p.T, p.rows, t0, (int)c0 + c, h, stage, lane);
+                    }
+                }
+                for (; c < cols; c += 16) {
                     uint32_t g[16], u[16];
                     tmem_ld16(tl + c, g);
                     tmem_ld16(tl + un.nt + c, u);
@@ -1036,7 +1103,7 @@ static cudaError_t run_pair(const GemmArgs& a, cudaStream_t s) {
     p.act = a.act;
     p.dtype = a.dtype;
     const int esz = a.dtype == MOE_F32 ? 4 : 2;
-    p.vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ldo * esz % 16 == 0 &&
+    p.vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ldo * esz % 16 == 0 && a.rows * esz % 16 == 0 &&
             (!a.acc || (reinterpret_cast<uintptr_t>(a.acc) % 16 == 0 && a.rows % 4 == 0));
     p.nt = MODE == kGated ? 128 : MODE == kMatmul ? 256 : P == 2 ? 128 : 64;
     p.tiles_r = ((MODE == kGated ? a.T : p.out_rows) + kPairRows - 1) / kPairRows;
@@ -1087,7 +1154,7 @@ static cudaError_t run_pair(const GemmArgs& a, cudaStream_t s) {
     else if (MODE != kGated)
         maps.small[1] = maps.small[0];
     const unsigned grid = 2 * (unsigned)(p.units < pairs ? p.units : pairs);
-    k_dense_pair<MODE, P, OT><<<grid, kPairThreads, kPairSmem, s>>>(maps, p);
+    k_dense_pair<MODE, P, OT><<<grid, kPairThreads, kPairSmem<MODE>, s>>>(maps, p);
     return cudaGetLastError();
 }
 

@@ -4,6 +4,7 @@
 // the weight scales and the bias).
 #include "moe_dense.cuh"
 #include "moe_device.cuh"
+#include "moe_ptx.cuh"
 
 namespace moe {
 namespace dense {
@@ -22,35 +23,55 @@ __device__ __forceinline__ uint32_t block_max_bits(uint32_t m, uint32_t* sh, int
     return __reduce_max_sync(kFull, lane < nw ? sh[buf * 32 + lane] : 0u);
 }
 
-// VEC consecutive elements of a row, in one load (the caller checked the alignment).
+// VEC consecutive elements of a row, in 16- or 8-byte loads (the caller checked the alignment).
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = to_f32(*p);
-    } else {
-        constexpr int kBytes = VEC * (int)sizeof(T);
-        static_assert(kBytes == 8 || kBytes == 16, "one load");
+struct Raw {
+    static constexpr int kWords = VEC * (int)sizeof(T) / 4;
+    union {
         T e[VEC];
-        if constexpr (kBytes == 16)
-            *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
-        else
-            *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+        uint32_t w[kWords > 0 ? kWords : 1];
+    };
+    __device__ __forceinline__ Raw() {}
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (VEC == 1) {
+            e[0] = *p;
+        } else if constexpr (kWords == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            w[0] = v.x;
+            w[1] = v.y;
+        } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = to_f32(e[i]);
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        }
     }
+    __device__ __forceinline__ T get(int i) const { return e[i]; }
+};
+
+// Byte K of four words, in order.
+template <int K>
+__device__ __forceinline__ uint32_t gather_byte(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t ab = __byte_perm(a, b, K | ((K + 4) << 4));
+    const uint32_t cd = __byte_perm(c, d, K | ((K + 4) << 4));
+    return __byte_perm(ab, cd, 0x5410);
 }
 
-// VEC int8 codes in one store.
-template <int VEC>
-__device__ __forceinline__ void store_codes(int8_t* p, const int (&c)[VEC]) {
+// Byte K of VEC words, XOR-ed with flip, as codes in one store.
+template <int VEC, int K>
+__device__ __forceinline__ void store_bytes(int8_t* p, const int (&c)[VEC], uint32_t flip) {
     if constexpr (VEC == 1) {
-        *p = (int8_t)c[0];
+        *p = (int8_t)(((uint32_t)c[0] >> (8 * K)) ^ (flip & 0xFFu));
     } else {
         uint32_t w[VEC / 4];
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i)
-            w[i] = (uint32_t)(c[4 * i] & 255) | ((uint32_t)(c[4 * i + 1] & 255) << 8) |
-                   ((uint32_t)(c[4 * i + 2] & 255) << 16) | ((uint32_t)c[4 * i + 3] << 24);
+            w[i] = gather_byte<K>((uint32_t)c[4 * i], (uint32_t)c[4 * i + 1], (uint32_t)c[4 * i + 2],
+                                  (uint32_t)c[4 * i + 3]) ^ flip;
         if constexpr (VEC == 4)
             *reinterpret_cast<uint32_t*>(p) = w[0];
         else
@@ -69,31 +90,40 @@ __device__ __forceinline__ void store_codes(int8_t* p, const int (&c)[VEC]) {
 constexpr int kQuantCache = 4;
 constexpr float kTinyRow = 1.925929944387236e-34f;  // 2^-112
 
+// round-half-away-from-zero of |v| < 2^23: adding half towards zero never
+// carries past an integer that v + half does not reach, and the conversion cuts
+// the rest.  (127 fl(1/d) d stays below 127.5, so no clamp is needed; 0 * inf
+// and NaN convert to 0.)
+__device__ __forceinline__ int round_away(float v) { return __float2int_rz(__fadd_rz(v, copysignf(0.5f, v))); }
+
 template <int DT, int VEC>
 __global__ void __launch_bounds__(512)
     k_quantize_token(const typename Elem<DT>::T* __restrict__ x, int64_t ldx, int cols, int8_t* __restrict__ q,
                      int64_t ldq, float* __restrict__ d) {
+    using T = typename Elem<DT>::T;
     __shared__ uint32_t sh[64];
     const int64_t row = blockIdx.x;
-    const auto* xr = x + row * ldx;
+    const T* xr = x + row * ldx;
     int8_t* qr = q + row * ldq;
     const int step = blockDim.x * VEC;
-    float v[kQuantCache][VEC];
+    Raw<T, VEC> v[kQuantCache];
     uint32_t m = 0;
+    auto peak = [&](const Raw<T, VEC>& r) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) m = max(m, __float_as_uint(to_f32(r.get(i))) & 0x7FFFFFFFu);
+    };
 #pragma unroll
     for (int j = 0; j < kQuantCache; ++j) {
-        const int c = (threadIdx.x + j * blockDim.x) * VEC;
-        if (c < cols) {
-            load_vec<typename Elem<DT>::T, VEC>(xr + c, v[j]);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) m = max(m, __float_as_uint(v[j][i]) & 0x7FFFFFFFu);
-        }
+        const int c = threadIdx.x * VEC + j * step;
+        if (c < cols) v[j].load(xr + c);
     }
-    for (int c = kQuantCache * step + threadIdx.x * VEC; c < cols; c += step) {
-        float e[VEC];
-        load_vec<typename Elem<DT>::T, VEC>(xr + c, e);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) m = max(m, __float_as_uint(e[i]) & 0x7FFFFFFFu);
+    for (int j = 0; j < kQuantCache; ++j)
+        if (threadIdx.x * VEC + j * step < cols) peak(v[j]);
+    for (int c = kQuantCache * step + threadIdx.x * VEC; c < cols; c += step) {
+        Raw<T, VEC> e;
+        e.load(xr + c);
+        peak(e);
     }
     m = block_max_bits(m, sh, 0);
     const float amax = __uint_as_float(m);
@@ -101,26 +131,21 @@ __global__ void __launch_bounds__(512)
     const float scale = live ? __fdiv_rn(amax, 127.0f) : 0.0f;
     const float inv = live ? __fdiv_rn(1.0f, scale) : 0.0f;
     if (threadIdx.x == 0) d[row] = m >= kInfBits ? __uint_as_float(0x7FC00000u) : scale;
-    auto code = [&](float f) {
-        return live ? (int)fminf(fmaxf(roundf(__fmul_rn(f, inv)), -127.0f), 127.0f) : 0;
+    auto put = [&](const Raw<T, VEC>& r, int c) {
+        int o[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o[i] = round_away(__fmul_rn(to_f32(r.get(i)), inv));
+        store_bytes<VEC, 0>(qr + c, o, 0u);
     };
 #pragma unroll
     for (int j = 0; j < kQuantCache; ++j) {
-        const int c = (threadIdx.x + j * blockDim.x) * VEC;
-        if (c < cols) {
-            int o[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = code(v[j][i]);
-            store_codes<VEC>(qr + c, o);
-        }
+        const int c = threadIdx.x * VEC + j * step;
+        if (c < cols) put(v[j], c);
     }
     for (int c = kQuantCache * step + threadIdx.x * VEC; c < cols; c += step) {
-        float e[VEC];
-        int o[VEC];
-        load_vec<typename Elem<DT>::T, VEC>(xr + c, e);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = code(e[i]);
-        store_codes<VEC>(qr + c, o);
+        Raw<T, VEC> e;
+        e.load(xr + c);
+        put(e, c);
     }
 }
 
@@ -176,165 +201,203 @@ struct GradRowsParams {
     int64_t pitch;
     RowScale* scale;
     float* partials;
+    bool bulk;  // rows of dy and acc start and end on 16 bytes
+};
+constexpr int kRowsAhead = 3;
+
+// What VEC columns of a row read.
+template <int MATS, int DT, int VEC>
+struct GradIn {
+    Raw<typename Elem<DT>::T, VEC> dy;
+    Raw<int32_t, VEC> acc[MATS];
+    __device__ __forceinline__ void load(const GradRowsParams& p, int64_t t, int c) {
+        dy.load(static_cast<const typename Elem<DT>::T*>(p.dy) + t * p.lddy + c);
+        if (MATS == 2 || p.acc) {
+#pragma unroll
+            for (int m = 0; m < MATS; ++m) acc[m].load(p.acc + ((int64_t)m * p.T + t) * p.N + c);
+        }
+    }
 };
 
-// The values and column contributions of VEC columns of row t.
+// Their values and column contributions.
 template <int MATS, int DT, int VEC>
-__device__ __forceinline__ void grad_cols(const GradRowsParams& p, int64_t t, int c, float xd, float (&v)[MATS][VEC],
+__device__ __forceinline__ void grad_cols(const GradRowsParams& p, const GradIn<MATS, DT, VEC>& in,
+                                          const Raw<float, VEC> (&sc)[MATS], float xd, float (&v)[MATS][VEC],
                                           float (&sum)[2][VEC]) {
-    float dy[VEC];
-    load_vec<typename Elem<DT>::T, VEC>(static_cast<const typename Elem<DT>::T*>(p.dy) + t * p.lddy + c, dy);
-    int a[MATS][VEC];
-#pragma unroll
-    for (int m = 0; m < MATS; ++m) {
-        if (MATS == 1 && !p.acc) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) a[m][i] = 0;
-            continue;
-        }
-        const int32_t* ap = p.acc + ((int64_t)m * p.T + t) * p.N + c;
-        if constexpr (VEC == 4)
-            *reinterpret_cast<int4*>(a[m]) = *reinterpret_cast<const int4*>(ap);
-        else
-            a[m][0] = *ap;
-    }
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        const float s0 = __ldg(p.s[0] + c + i);
+        const float dy = to_f32(in.dy.get(i));
+        const float s0 = sc[0].get(i);
         if constexpr (MATS == 2) {
-            const float s1 = __ldg(p.s[1] + c + i);
-            const float xg = xd * (float)a[0][i], xu = xd * (float)a[1][i];
+            const float s1 = sc[MATS - 1].get(i);
+            const float xg = xd * (float)in.acc[0].get(i), xu = xd * (float)in.acc[MATS - 1].get(i);
             float act, dact;
             act_value_grad(p.act, xg * s0, act, dact);
-            const float dg = dy[i] * (xu * s1) * dact, du = dy[i] * act;
+            const float dg = dy * (xu * s1) * dact, du = dy * act;
             v[0][i] = dg * s0;
-            v[1][i] = du * s1;
+            v[MATS - 1][i] = du * s1;
             sum[0][i] += dg * xg;
             sum[1][i] += du * xu;
         } else {
-            v[0][i] = dy[i] * s0;
-            sum[0][i] += dy[i] * (xd * (float)a[0][i]);
-            sum[1][i] += dy[i];
+            v[0][i] = dy * s0;
+            if (p.acc) sum[0][i] += dy * (xd * (float)in.acc[0].get(i));
+            sum[1][i] += dy;
         }
     }
 }
 
-// The digits of VEC values into the row's planes.
+// The digits of VEC values into the row's planes.  Adding 128 to each of the
+// lower digits' places turns the signed digits into the bytes of one integer,
+// off by their top bit.
 template <int P, int VEC>
 __device__ __forceinline__ void store_planes(const GradRowsParams& p, int64_t t, int m, int c, int mats, float pre,
                                              float inv, const float (&v)[VEC]) {
-    int dig[P][VEC];
+    int r[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        // the clamp holds the one value that rounding may lift past the top digit
-        int r = __float2int_rn(fminf(fmaxf(v[i] * pre * inv, -kPlaneMax<P>), kPlaneMax<P>));
-#pragma unroll
-        for (int k = 0; k < P; ++k) {
-            dig[k][i] = (int)(int8_t)r;
-            r = (r - dig[k][i]) >> 8;
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < P; ++k)
-        store_codes<VEC>(p.planes + ((int64_t)k * p.T + t) * (mats * p.pitch) + m * p.pitch + c, dig[k]);
+    for (int i = 0; i < VEC; ++i) r[i] = __float2int_rn(v[i] * pre * inv) + (P == 2 ? 0x8080 : 0x808080);
+    const int64_t row = mats * p.pitch;
+    int8_t* o = p.planes + t * row + m * p.pitch + c;
+    store_bytes<VEC, 0>(o, r, 0x80808080u);
+    store_bytes<VEC, 1>(o + p.T * row, r, 0x80808080u);
+    if constexpr (P == 3) store_bytes<VEC, 2>(o + 2 * p.T * row, r, 0x80808080u);
 }
 
-// NJ > 0: a thread owns NJ groups of VEC columns, kept in registers; NJ = 0:
-// any number of columns, computed twice, with the column sums in the partials.
+template <int MATS, int VEC>
+__device__ __forceinline__ void peak_of(const float (&v)[MATS][VEC], uint32_t& m) {
+#pragma unroll
+    for (int k = 0; k < MATS; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) m = max(m, __float_as_uint(v[k][i]) & 0x7FFFFFFFu);
+}
+
+// The fixed point of a row from its largest magnitude.  A row with an infinity
+// or a NaN has none: its scale is NaN and its digits are zero.  Tiny rows are
+// lifted by 2^64 first, so that D / m stays finite and m / D a normal number.
+template <int P>
+__device__ __forceinline__ bool fixed_point(uint32_t m, float& pre, float& inv, RowScale& scale) {
+    const bool finite = m < kInfBits;
+    const float mx = __uint_as_float(m);
+    pre = mx < 8.673617379884035e-19f ? 1.8446744073709552e19f : 1.0f;  // 2^-60, 2^64
+    const float mp = mx * pre;
+    const bool live = finite && mp > 0.0f;
+    inv = live ? __fdiv_rn(kPlaneMax<P>, mp) : 0.0f;
+    scale = RowScale{finite ? __fdiv_rn(mp, kPlaneMax<P>) : __uint_as_float(0x7FC00000u), 1.0f / pre};
+    return live;
+}
+
+// A thread owns NJ groups of VEC columns; the next row's loads are in flight
+// while a row waits for its largest value.
 template <int MATS, int DT, int VEC, int NJ>
-__global__ void __launch_bounds__(NJ == 4 ? 512 : 256) k_grad_rows(const GradRowsParams p) {
+__global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_grad_rows(const GradRowsParams p) {
     constexpr int P = planes_of(DT);
     __shared__ uint32_t sh[64];
-    constexpr int kN = NJ > 0 ? NJ : 1;
-    float v[kN][MATS][VEC];
-    float sum[kN][2][VEC];
+    GradIn<MATS, DT, VEC> in[NJ];
+    Raw<float, VEC> sc[NJ][MATS];
+    float sum[NJ][2][VEC], xd_next = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kN; ++j)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) sum[j][0][i] = sum[j][1][i] = 0.0f;
+    auto col = [&](int j) { return (int)(threadIdx.x + j * blockDim.x) * VEC; };
+    auto fetch = [&](int64_t t) {
+        if (p.xd) xd_next = p.xd[t];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            if (col(j) < p.N) in[j].load(p, t, col(j));
+    };
+    // rows further ahead are asked into L2 (whole rows on the 16-byte grid)
+    auto ahead = [&](int64_t t) {
+        if (VEC == 1 || !p.bulk || threadIdx.x != 0 || t >= p.T) return;
+        using T = typename Elem<DT>::T;
+        bulk_prefetch_l2(static_cast<const T*>(p.dy) + t * p.lddy, p.N * (uint32_t)sizeof(T));
+        if (MATS == 2 || p.acc)
+#pragma unroll
+            for (int m = 0; m < MATS; ++m) bulk_prefetch_l2(p.acc + ((int64_t)m * p.T + t) * p.N, p.N * 4u);
+    };
+    int buf = 0;
+    fetch(blockIdx.x);
+    for (int i = 1; i <= kRowsAhead; ++i) ahead(blockIdx.x + (int64_t)i * gridDim.x);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+        if (col(j) < p.N)
+#pragma unroll
+            for (int m = 0; m < MATS; ++m) sc[j][m].load(p.s[m] + col(j));
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
+        const float xd = xd_next;
+        ahead(t + (int64_t)(kRowsAhead + 1) * gridDim.x);
+        float v[NJ][MATS][VEC];
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            if (col(j) < p.N) {
+                grad_cols<MATS, DT, VEC>(p, in[j], sc[j], xd, v[j], sum[j]);
+                peak_of<MATS, VEC>(v[j], m);
+            }
+        if (t + gridDim.x < p.T) fetch(t + gridDim.x);
+        m = block_max_bits(m, sh, buf);
+        float pre, inv;
+        RowScale scale;
+        const bool live = fixed_point<P>(m, pre, inv, scale);
+        if (threadIdx.x == 0) p.scale[t] = scale;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            if (col(j) < p.N)
+#pragma unroll
+                for (int k = 0; k < MATS; ++k) {
+                    if (!live)
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) v[j][k][i] = 0.0f;
+                    store_planes<P, VEC>(p, t, k, col(j), MATS, pre, inv, v[j][k]);
+                }
+    }
+    float* part = p.partials + (int64_t)blockIdx.x * 2 * p.N;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+        if (col(j) < p.N)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) part[(int64_t)k * p.N + col(j) + i] = sum[j][k][i];
+}
+
+// Rows of any length: the values are computed twice and the column sums kept
+// in the CTA's partials.
+template <int MATS, int DT>
+__global__ void __launch_bounds__(1024) k_grad_rows_long(const GradRowsParams p) {
+    constexpr int P = planes_of(DT);
+    __shared__ uint32_t sh[64];
     float* part = p.partials + (int64_t)blockIdx.x * 2 * p.N;
     int buf = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
         const float xd = p.xd ? p.xd[t] : 0.0f;
         uint32_t m = 0;
-        if constexpr (NJ > 0) {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int c = (threadIdx.x + j * blockDim.x) * VEC;
-                if (c < p.N) {
-                    grad_cols<MATS, DT, VEC>(p, t, c, xd, v[j], sum[j]);
-#pragma unroll
-                    for (int k = 0; k < MATS; ++k)
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) m = max(m, __float_as_uint(v[j][k][i]) & 0x7FFFFFFFu);
-                }
-            }
-        } else {
-            for (int c = threadIdx.x * VEC; c < p.N; c += blockDim.x * VEC) {
-                const bool first = t == blockIdx.x;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) sum[0][k][i] = first ? 0.0f : part[(int64_t)k * p.N + c + i];
-                grad_cols<MATS, DT, VEC>(p, t, c, xd, v[0], sum[0]);
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) part[(int64_t)k * p.N + c + i] = sum[0][k][i];
-#pragma unroll
-                for (int k = 0; k < MATS; ++k)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) m = max(m, __float_as_uint(v[0][k][i]) & 0x7FFFFFFFu);
-            }
+        for (int c = threadIdx.x; c < p.N; c += blockDim.x) {
+            GradIn<MATS, DT, 1> in;
+            float v[MATS][1], sum[2][1];
+            Raw<float, 1> sc[MATS];
+            for (int k = 0; k < MATS; ++k) sc[k].load(p.s[k] + c);
+            for (int k = 0; k < 2; ++k) sum[k][0] = t == blockIdx.x ? 0.0f : part[(int64_t)k * p.N + c];
+            in.load(p, t, c);
+            grad_cols<MATS, DT, 1>(p, in, sc, xd, v, sum);
+            peak_of<MATS, 1>(v, m);
+            for (int k = 0; k < 2; ++k) part[(int64_t)k * p.N + c] = sum[k][0];
         }
         m = block_max_bits(m, sh, buf);
-        // A row with an infinity or a NaN has no fixed point: its scale is NaN
-        // and its digits zero.  Tiny rows are lifted by 2^64 first, so that
-        // D / m stays finite and m / D a normal number.
-        const bool finite = m < kInfBits;
-        const float mx = __uint_as_float(m);
-        const float pre = mx < 8.673617379884035e-19f ? 1.8446744073709552e19f : 1.0f;  // 2^-60, 2^64
-        const float mp = mx * pre;
-        const bool live = finite && mp > 0.0f;
-        const float inv = live ? __fdiv_rn(kPlaneMax<P>, mp) : 0.0f;
-        if (threadIdx.x == 0)
-            p.scale[t] = RowScale{finite ? __fdiv_rn(mp, kPlaneMax<P>) : __uint_as_float(0x7FC00000u), 1.0f / pre};
-        if constexpr (NJ > 0) {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int c = (threadIdx.x + j * blockDim.x) * VEC;
-                if (c < p.N) {
-#pragma unroll
-                    for (int k = 0; k < MATS; ++k) {
-                        if (!live)
-#pragma unroll
-                            for (int i = 0; i < VEC; ++i) v[j][k][i] = 0.0f;
-                        store_planes<P, VEC>(p, t, k, c, MATS, pre, inv, v[j][k]);
-                    }
-                }
+        float pre, inv;
+        RowScale scale;
+        const bool live = fixed_point<P>(m, pre, inv, scale);
+        if (threadIdx.x == 0) p.scale[t] = scale;
+        for (int c = threadIdx.x; c < p.N; c += blockDim.x) {
+            GradIn<MATS, DT, 1> in;
+            float v[MATS][1], sum[2][1] = {{0.0f}, {0.0f}};
+            Raw<float, 1> sc[MATS];
+            for (int k = 0; k < MATS; ++k) sc[k].load(p.s[k] + c);
+            in.load(p, t, c);
+            grad_cols<MATS, DT, 1>(p, in, sc, xd, v, sum);
+            for (int k = 0; k < MATS; ++k) {
+                if (!live) v[k][0] = 0.0f;
+                store_planes<P, 1>(p, t, k, c, MATS, pre, inv, v[k]);
             }
-        } else {
-            for (int c = threadIdx.x * VEC; c < p.N; c += blockDim.x * VEC) {
-                grad_cols<MATS, DT, VEC>(p, t, c, xd, v[0], sum[0]);
-#pragma unroll
-                for (int k = 0; k < MATS; ++k) {
-                    if (!live)
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) v[0][k][i] = 0.0f;
-                    store_planes<P, VEC>(p, t, k, c, MATS, pre, inv, v[0][k]);
-                }
-            }
-        }
-    }
-    if constexpr (NJ > 0) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int c = (threadIdx.x + j * blockDim.x) * VEC;
-            if (c < p.N)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) part[(int64_t)k * p.N + c + i] = sum[j][k][i];
         }
     }
 }
@@ -359,34 +422,39 @@ __global__ void __launch_bounds__(1024) k_col_sums(const float* __restrict__ par
     }
 }
 
-// CTAs of the gradient row kernel: enough to fill the SMs four times over (the
-// rows of one CTA wait for its barrier; the others run meanwhile).
+// CTAs of the gradient row kernel: a fixed grid (the column sums' order is the
+// same from call to call), at most four an SM.
 int grad_rows_grid(int T) {
     const int most = 4 * device_info().sm_count;
     return T < most ? T : most;
 }
 
-template <int MATS, int DT, int VEC>
-static cudaError_t grad_rows(const GradRowsParams& p, int grid, cudaStream_t s) {
-    const int groups = (p.N + VEC - 1) / VEC;
-    const int threads = groups >= 256 ? 256 : (groups + 31) / 32 * 32;
-    if (groups <= 256)
-        k_grad_rows<MATS, DT, VEC, 1><<<grid, threads, 0, s>>>(p);
-    else if (groups <= 512)
-        k_grad_rows<MATS, DT, VEC, 2><<<grid, 256, 0, s>>>(p);
-    else if (groups <= 2048)
-        k_grad_rows<MATS, DT, VEC, 4><<<grid, (groups + 127) / 128 * 32, 0, s>>>(p);
-    else
-        k_grad_rows<MATS, DT, VEC, 0><<<grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
-}
-
 template <int MATS, int DT>
-static cudaError_t grad_rows_dt(const GradRowsArgs& a, const GradRowsParams& p, int grid, cudaStream_t s) {
+static cudaError_t grad_rows(const GradRowsArgs& a, GradRowsParams p, int& grid, cudaStream_t s) {
     const size_t vb = 4 * sizeof(typename Elem<DT>::T);
-    const bool vec = reinterpret_cast<uintptr_t>(a.dy) % vb == 0 && a.lddy % 4 == 0 && a.N % 4 == 0 &&
-                     reinterpret_cast<uintptr_t>(a.acc) % 16 == 0;
-    return vec ? grad_rows<MATS, DT, 4>(p, grid, s) : grad_rows<MATS, DT, 1>(p, grid, s);
+    bool vec = reinterpret_cast<uintptr_t>(a.dy) % vb == 0 && a.lddy % 4 == 0 && a.N % 4 == 0 &&
+               reinterpret_cast<uintptr_t>(a.acc) % 16 == 0;
+    for (int m = 0; m < MATS; ++m) vec = vec && reinterpret_cast<uintptr_t>(a.s[m]) % 16 == 0;
+    const int esz = (int)sizeof(typename Elem<DT>::T);
+    p.bulk = vec && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && a.lddy * esz % 16 == 0 && a.N * esz % 16 == 0;
+    const int groups = vec ? a.N / 4 : a.N;
+    // two groups of four columns a thread where 768 threads suffice (85
+    // registers each), four up to 512 threads; single columns one or four
+    const int per = vec ? (groups <= 2 * 768 ? 2 : 4) : (groups <= 512 ? 1 : 4);
+    const int threads = (groups + 32 * per - 1) / (32 * per) * 32;
+    if (threads > (vec ? (per == 2 ? 768 : 512) : 1024)) {
+        k_grad_rows_long<MATS, DT><<<grid, 1024, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    const int per_sm = threads > 384 ? 1 : threads > 256 ? 2 : threads > 192 ? 3 : 4;
+    if (grid > per_sm * device_info().sm_count) grid = per_sm * device_info().sm_count;
+    if (vec)
+        per == 2 ? k_grad_rows<MATS, DT, 4, 2><<<grid, threads, 0, s>>>(p)
+                 : k_grad_rows<MATS, DT, 4, 4><<<grid, threads, 0, s>>>(p);
+    else
+        per == 1 ? k_grad_rows<MATS, DT, 1, 1><<<grid, threads, 0, s>>>(p)
+                 : k_grad_rows<MATS, DT, 1, 4><<<grid, threads, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_grad_rows(const GradRowsArgs& a, cudaStream_t s) {
@@ -404,16 +472,16 @@ cudaError_t launch_grad_rows(const GradRowsArgs& a, cudaStream_t s) {
     p.pitch = a.pitch;
     p.scale = a.scale;
     p.partials = a.partials;
-    const int grid = grad_rows_grid(a.T);
+    int grid = grad_rows_grid(a.T);
     cudaError_t e;
     if (a.n_mats == 2)
-        e = a.dtype == MOE_F32    ? grad_rows_dt<2, MOE_F32>(a, p, grid, s)
-            : a.dtype == MOE_BF16 ? grad_rows_dt<2, MOE_BF16>(a, p, grid, s)
-                                  : grad_rows_dt<2, MOE_F16>(a, p, grid, s);
+        e = a.dtype == MOE_F32    ? grad_rows<2, MOE_F32>(a, p, grid, s)
+            : a.dtype == MOE_BF16 ? grad_rows<2, MOE_BF16>(a, p, grid, s)
+                                  : grad_rows<2, MOE_F16>(a, p, grid, s);
     else
-        e = a.dtype == MOE_F32    ? grad_rows_dt<1, MOE_F32>(a, p, grid, s)
-            : a.dtype == MOE_BF16 ? grad_rows_dt<1, MOE_BF16>(a, p, grid, s)
-                                  : grad_rows_dt<1, MOE_F16>(a, p, grid, s);
+        e = a.dtype == MOE_F32    ? grad_rows<1, MOE_F32>(a, p, grid, s)
+            : a.dtype == MOE_BF16 ? grad_rows<1, MOE_BF16>(a, p, grid, s)
+                                  : grad_rows<1, MOE_F16>(a, p, grid, s);
     if (e != cudaSuccess || (!a.colsum[0] && !a.colsum[1])) return e;
     k_col_sums<<<dim3((unsigned)((a.N + 31) / 32), 2), 1024, 0, s>>>(p.partials, grid, a.N, a.colsum[0], a.colsum[1]);
     return cudaGetLastError();

@@ -10,7 +10,7 @@ Bounds (u = 2^-24, half a step of fp32; e(t) = eps/2 of the result's type):
     than 24 u.  |delta act| <= |act| (24 + 16 |z|) u, and the same for each
     addend of its derivative.
   gradient rows: an element v is off by its own arithmetic, delta_v, and by the
-    fixed point: at most m / (2 D) (m: the row's largest; D: 32639 or 8355711),
+    fixed point: at most m / (2 D) (m: the row's largest; D: 32639 or 8355600),
     and 2u of v from the scaling.  dx then has sum |w| of these, and 8u sum |w v|
     from the join of the digits and the scales.
   column sums: each term's own error, and one rounding for each of the rows that
@@ -82,7 +82,7 @@ def ref_gated(x, xd, ws, ss, act, dtype):
 
 
 def _dx(vs, evs, ws, dtype):
-    D = 8355711.0 if dtype == torch.float32 else 32639.0
+    D = 8355600.0 if dtype == torch.float32 else 32639.0
     m = torch.stack([v.abs().amax(1) for v in vs]).amax(0)[:, None]
     dx = sum(v @ w.double() for v, w in zip(vs, ws))
     tol = sum((ev + 10 * U * v.abs() + 0.51 * m / D) @ w.double().abs() for v, ev, w in zip(vs, evs, ws))
