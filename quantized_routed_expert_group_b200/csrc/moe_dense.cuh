@@ -70,7 +70,11 @@ __device__ __forceinline__ void store_elem(void* out, int64_t i, int dtype, floa
 // act(g) = g sigmoid(z(g)): z = g (SiLU), z = 2 sqrt(2/pi)(g + 0.044715 g^3)
 // (the tanh form of GELU, since (1 + tanh y)/2 = sigmoid(2 y); written so, it
 // does not cancel for negative g).  With e = exp(-|z|) <= 1 nothing overflows:
-// sigmoid(z) is 1/(1+e) or e/(1+e), and its derivative e/(1+e)^2.
+// sigmoid(z) is 1/(1+e) or e/(1+e), and its derivative e/(1+e)^2.  The
+// reciprocal of 1 + e, in [1, 2], is the intrinsic good to two units in the last
+// place: the exactly rounded one branches, which keeps the values of a thread
+// from overlapping (the gated product's epilogue took 18,000 cycles a tile with
+// it).
 // ---------------------------------------------------------------------------
 constexpr float kGelu0 = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGelu1 = 0.044715f;
@@ -78,7 +82,7 @@ constexpr float kGelu1 = 0.044715f;
 __device__ __forceinline__ float act_value(int act, float g) {
     const float z = act == MOE_ACT_SILU ? g : kGelu0 * (g + kGelu1 * g * g * g);
     const float e = expf(-fabsf(z));
-    const float r = __frcp_rn(1.0f + e);
+    const float r = __fdividef(1.0f, 1.0f + e);
     return g * (z >= 0.0f ? r : e * r);
 }
 
@@ -86,12 +90,97 @@ __device__ __forceinline__ void act_value_grad(int act, float g, float& a, float
     const float z = act == MOE_ACT_SILU ? g : kGelu0 * (g + kGelu1 * g * g * g);
     const float dz = act == MOE_ACT_SILU ? 1.0f : kGelu0 * (1.0f + 3.0f * kGelu1 * g * g);
     const float e = expf(-fabsf(z));
-    const float r = __frcp_rn(1.0f + e);
+    const float r = __fdividef(1.0f, 1.0f + e);
     const float sig = z >= 0.0f ? r : e * r;
     const float dsig = e * r * r;
     a = g * sig;
     // far out the derivative of the sigmoid is zero while dz may be infinite
     da = sig + (dsig == 0.0f ? 0.0f : g * dsig * dz);
+}
+
+// ---------------------------------------------------------------------------
+// The per-token quantiser's arithmetic.  From the bits of a row's largest
+// magnitude: d = amax / 127 and 1/d.  Rows below 2^-112 store zeros (so d is a
+// normal number and 1/d finite); a row with an infinity or a NaN stores d = NaN,
+// so that whatever is computed from it says so.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kInfBits = 0x7F800000u;
+constexpr float kTinyRow = 1.925929944387236e-34f;  // 2^-112
+
+struct QuantScale {
+    float scale, inv;
+};
+
+__device__ __forceinline__ QuantScale quant_scale(uint32_t peak_bits) {
+    const float amax = __uint_as_float(peak_bits);
+    const bool live = peak_bits < kInfBits && amax >= kTinyRow;
+    const float d = live ? __fdiv_rn(amax, 127.0f) : 0.0f;
+    return QuantScale{peak_bits >= kInfBits ? __uint_as_float(0x7FC00000u) : d, live ? __fdiv_rn(1.0f, d) : 0.0f};
+}
+
+// round-half-away-from-zero of |v| < 2^23: adding half towards zero never
+// carries past an integer that v + half does not reach, and the conversion cuts
+// the rest.  (amax times fl(1/d) stays below 127.5, so codes need no clamp;
+// 0 * inf and NaN convert to 0.)
+__device__ __forceinline__ int round_away(float v) { return __float2int_rz(__fadd_rz(v, copysignf(0.5f, v))); }
+
+// ---------------------------------------------------------------------------
+// Vectors of a row's elements and codes
+// ---------------------------------------------------------------------------
+// VEC consecutive elements of a row, in 16- or 8-byte loads (the caller checked the alignment).
+template <typename T, int VEC>
+struct Raw {
+    static constexpr int kWords = VEC * (int)sizeof(T) / 4;
+    union {
+        T e[VEC];
+        uint32_t w[kWords > 0 ? kWords : 1];
+    };
+    __device__ __forceinline__ Raw() {}
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (VEC == 1) {
+            e[0] = *p;
+        } else if constexpr (kWords == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            w[0] = v.x;
+            w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ T get(int i) const { return e[i]; }
+};
+
+// Byte K of four words, in order.
+template <int K>
+__device__ __forceinline__ uint32_t gather_byte(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t ab = __byte_perm(a, b, K | ((K + 4) << 4));
+    const uint32_t cd = __byte_perm(c, d, K | ((K + 4) << 4));
+    return __byte_perm(ab, cd, 0x5410);
+}
+
+// Byte K of VEC words, XOR-ed with flip, as codes in one store.
+template <int VEC, int K>
+__device__ __forceinline__ void store_bytes(int8_t* p, const int (&c)[VEC], uint32_t flip) {
+    if constexpr (VEC == 1) {
+        *p = (int8_t)(((uint32_t)c[0] >> (8 * K)) ^ (flip & 0xFFu));
+    } else {
+        uint32_t w[VEC / 4];
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i)
+            w[i] = gather_byte<K>((uint32_t)c[4 * i], (uint32_t)c[4 * i + 1], (uint32_t)c[4 * i + 2],
+                                  (uint32_t)c[4 * i + 3]) ^ flip;
+        if constexpr (VEC == 4)
+            *reinterpret_cast<uint32_t*>(p) = w[0];
+        else
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -147,6 +236,12 @@ struct GemmArgs {
 
 cudaError_t launch_matmul(const GemmArgs& a, cudaStream_t s);
 cudaError_t launch_gated(const GemmArgs& a, cudaStream_t s);
+// The products of up to a few float tokens (rows of x with stride a.ldx, type
+// x_type), quantised inside the kernel; for operands that few_quantised_fits.
+// dependent: the kernel may start while the one before it on the stream ends.
+bool few_quantised_fits(const GemmArgs& a, const void* x, int x_type);
+cudaError_t launch_matmul_quantised(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s);
+cudaError_t launch_gated_quantised(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s);
 cudaError_t launch_grad_matmul(const GemmArgs& a, cudaStream_t s);
 cudaError_t read_device_error(cudaStream_t s, int32_t* code);
 

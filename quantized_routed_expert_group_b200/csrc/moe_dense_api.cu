@@ -296,6 +296,36 @@ MOE_API int moe_dense_ffn(const void* x, int dtype, int64_t ldx, int T, int hidd
     int8_t* hq = reinterpret_cast<int8_t*>(ws + L.hq);
     float* hd = reinterpret_cast<float*>(ws + L.hd);
     const NvtxRange range("moe/dense_ffn");
+    GemmArgs a{}, b{};
+    a.w[0] = experts->w_gate;
+    a.w[1] = experts->w_up;
+    a.s[0] = experts->s_gate;
+    a.s[1] = experts->s_up;
+    a.ldw[0] = a.ldw[1] = a.cols = hidden;
+    a.n_mats = 2;
+    a.rows = inter;
+    a.ldx = ldx;
+    a.T = T;
+    a.act = act;
+    a.out = h;
+    a.ldo = L.ldh;
+    a.dtype = MOE_F32;
+    b.w[0] = experts->w_down;
+    b.s[0] = experts->s_down;
+    b.ldw[0] = b.cols = inter;
+    b.n_mats = 1;
+    b.rows = hidden;
+    b.ldx = L.ldh;
+    b.T = T;
+    b.out = out;
+    b.ldo = ldo;
+    b.dtype = dtype;
+    if (few_quantised_fits(a, x, dtype) && few_quantised_fits(b, h, MOE_F32)) {
+        // a few tokens: each product quantises its own input, two launches
+        st = status_of(launch_gated_quantised(a, x, dtype, false, (cudaStream_t)stream));
+        if (!st) st = status_of(launch_matmul_quantised(b, h, MOE_F32, true, (cudaStream_t)stream));
+        return st;
+    }
     st = moe_quantize_act_token(x, dtype, T, hidden, ldx, xq, L.ldx, xd, stream);
     if (!st)
         st = moe_gated_ffn(xq, L.ldx, xd, T, experts->w_gate, hidden, experts->s_gate, experts->w_up, hidden,

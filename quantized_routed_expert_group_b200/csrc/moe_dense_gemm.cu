@@ -410,20 +410,28 @@ __global__ void __launch_bounds__(kTileThreads)
 }
 
 // ---------------------------------------------------------------------------
-// A few tokens: integer dots on the CUDA cores
+// A few tokens: the weights' stream
 // ---------------------------------------------------------------------------
-// With up to TN tokens the products stream the weights once and do a few
-// dp4a per loaded word: a row (gated: its gate and up rows) is read by `wpr`
-// warps of one CTA, each lane taking every (32 wpr)-th 16-byte chunk with
-// kUnroll of them in flight, and the warps' sums meet in shared memory.  The
-// tokens' codes come through L1.  More warps share a row when the rows alone do
-// not fill the SMs.
-constexpr int kDotThreads = 256;
+// With up to 16 tokens the products read every weight once and little else, so
+// what counts is bytes in flight and few instructions for each.  A CTA takes 16
+// rows (gated: of both matrices), its warps every kWarps-th 64-byte column of
+// them: a lane loads 16 bytes of two rows straight into the A fragments of two
+// m16n8k32 products (the order of k inside a fragment is free as long as the
+// tokens' B fragments use the same), with kUnroll columns under way.  Up to 8
+// tokens cost what one does.  The warps' integer sums meet in shared memory.
+// (The tcgen05 kernels need a tile of 128 rows in shared memory first; here that
+// detour costs more than the products.)
+//
+// With QUANT the tokens come as floats: every CTA quantises all of them into
+// shared memory, with the arithmetic of k_quantize_token, while its first
+// weights are under way; that saves a launch and a trip through L2.
+constexpr int kFewTokens = 16;
+constexpr int kFewRows = 16;
 
-struct DotParams {
+struct FewParams {
     const uint8_t* w[kMaxMats];
     int64_t ldw[kMaxMats];
-    const uint8_t* x;
+    const void* x;
     int64_t ldx;
     const float* xd;
     const float* s[kMaxMats];
@@ -432,100 +440,145 @@ struct DotParams {
     int64_t ldo;
     int32_t* acc;
     int T, rows, cols;
-    int wpr;  // warps of a row: 1, 2, 4 or 8
+    int pitch;   // QUANT: bytes of a token's codes in shared memory
     int act, dtype;
     int w_unit[kMaxMats], x_unit;
+    bool dependent;  // launched early: wait for the kernel before it
 };
 
-__device__ __forceinline__ int dot16(const uint4 a, const uint4 b, int c) {
-    c = __dp4a((int)a.x, (int)b.x, c);
-    c = __dp4a((int)a.y, (int)b.y, c);
-    c = __dp4a((int)a.z, (int)b.z, c);
-    return __dp4a((int)a.w, (int)b.w, c);
+__device__ __forceinline__ void mma_16832(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// FAST: rows on the 16-byte grid, full chunks read with 16-byte loads.
-template <int MODE, int TN, bool FAST>
-__global__ void __launch_bounds__(kDotThreads) k_dense_dot(const DotParams p) {
+// XT: int8_t codes, or the type of tokens to quantise.  NB: blocks of 8 tokens.
+// FAST: weight rows (and codes) on the 16-byte grid and cols a multiple of 16.
+template <int MODE, int NB, typename XT, bool FAST, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) k_dense_few(const FewParams p) {
     constexpr int M = MODE == kGated ? 2 : 1;
-    constexpr int kUnroll = FAST ? (TN == 1 ? 6 : TN == 2 ? 4 : 2) : 1;
-    __shared__ int sh[8][M * TN];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rpc = 8 / p.wpr;  // rows of a CTA
-    const int64_t row = (int64_t)blockIdx.x * rpc + warp / p.wpr;
-    const int sub = warp % p.wpr;
-    int v[M][TN];
+    constexpr bool QUANT = sizeof(XT) > 1;
+    constexpr int kUnroll = FAST ? (M == 2 ? 4 : 6) : 1;
+    extern __shared__ __align__(16) uint8_t few_smem[];
+    int* red = reinterpret_cast<int*>(few_smem);  // [WARPS][M][NB][128]
+    uint32_t* peak = reinterpret_cast<uint32_t*>(few_smem + WARPS * M * NB * 512);  // QUANT: [8 NB]
+    uint8_t* codes = reinterpret_cast<uint8_t*>(peak + 8 * NB);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int64_t row0 = (int64_t)blockIdx.x * kFewRows;
+    const int nch = (p.cols + 63) / 64;
+    const uint8_t* wr[M][2];
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int t = 0; t < TN; ++t) v[m][t] = 0;
-    if (row < p.rows) {
-        const uint8_t* wr[M];
+        for (int h = 0; h < 2; ++h) wr[m][h] = p.w[m] + min(row0 + g + 8 * h, (int64_t)p.rows - 1) * p.ldw[m];
+    uint4 a[kUnroll][M][2];
+    auto load_w = [&](int ch) {
 #pragma unroll
-        for (int m = 0; m < M; ++m) wr[m] = p.w[m] + row * p.ldw[m];
-        const int chunks = p.cols / 16, step = 32 * p.wpr;
-        int c = lane + 32 * sub;
-        if constexpr (FAST) {
-            for (; c < chunks; c += kUnroll * step) {
-                uint4 a[kUnroll][M];
+        for (int u = 0; u < kUnroll; ++u) {
+            const int c = (ch + u * WARPS) * 64 + 16 * q;
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u)
+            for (int m = 0; m < M; ++m)
 #pragma unroll
-                    for (int m = 0; m < M; ++m) {
-                        const int cu = c + u * step;
-                        a[u][m] = cu < chunks ? ld_stream_v4(wr[m] + 16 * (int64_t)cu) : make_uint4(0, 0, 0, 0);
-                    }
+                for (int h = 0; h < 2; ++h)
+                    a[u][m][h] = c >= p.cols ? make_uint4(0, 0, 0, 0)
+                                 : FAST      ? ld_stream_v4(wr[m][h] + c)
+                                             : load16(wr[m][h], c, p.cols, p.w_unit[m]);
+        }
+    };
+    load_w(warp);
+    if constexpr (QUANT) {
+        if (p.dependent) pdl_wait();
+        if (threadIdx.x < 8 * NB) peak[threadIdx.x] = 0;
+        __syncthreads();
+        constexpr int V = 16 / (int)sizeof(XT);
+        const XT* x = static_cast<const XT*>(p.x);
+        for (int t = 0; t < p.T; ++t) {
+            uint32_t m = 0;
+            for (int c = V * threadIdx.x; c < p.cols; c += 32 * V * WARPS) {
+                Raw<XT, V> e;
+                e.load(x + t * p.ldx + c);
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int cu = min(c + u * step, chunks - 1);
+                for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(to_f32(e.get(i))) & 0x7FFFFFFFu);
+            }
+            m = __reduce_max_sync(kFull, m);
+            if (lane == 0) atomicMax(&peak[t], m);
+        }
+        __syncthreads();
+        for (int t = 0; t < p.T; ++t) {
+            const float inv = quant_scale(peak[t]).inv;
+            for (int c = V * threadIdx.x; c < p.cols; c += 32 * V * WARPS) {
+                Raw<XT, V> e;
+                int o[V];
+                e.load(x + t * p.ldx + c);
 #pragma unroll
-                    for (int t = 0; t < TN; ++t) {
-                        const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.x + min(t, p.T - 1) * p.ldx) + cu);
+                for (int i = 0; i < V; ++i) o[i] = round_away(__fmul_rn(to_f32(e.get(i)), inv));
+                store_bytes<V, 0>(reinterpret_cast<int8_t*>(codes) + t * p.pitch + c, o, 0u);
+            }
+        }
+        __syncthreads();
+    }
+    int acc[M][NB][4];
 #pragma unroll
-                        for (int m = 0; m < M; ++m) v[m][t] = dot16(a[u][m], b, v[m][t]);
-                    }
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][n][i] = 0;
+    for (int ch = warp; ch < nch; ch += kUnroll * WARPS) {
+        if (ch > warp) load_w(ch);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int c = (ch + u * WARPS) * 64 + 16 * q;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const int t = 8 * n + g;
+                uint4 b = make_uint4(0, 0, 0, 0);
+                if (t < p.T && c < p.cols) {
+                    if constexpr (QUANT)
+                        b = *reinterpret_cast<const uint4*>(codes + t * p.pitch + c);
+                    else
+                        b = FAST ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + t * p.ldx + c))
+                                 : load16(static_cast<const uint8_t*>(p.x) + t * p.ldx, c, p.cols, p.x_unit);
+                }
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const uint4 lo = a[u][m][0], hi = a[u][m][1];
+                    mma_16832(acc[m][n], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+                    mma_16832(acc[m][n], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
                 }
             }
         }
-        // the row's last bytes; the whole row when it is off the grid
-        for (c = FAST ? chunks + lane + 32 * sub : lane + 32 * sub; c * 16 < p.cols; c += step) {
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const uint4 a = load16(wr[m], (int64_t)c * 16, p.cols, p.w_unit[m]);
-#pragma unroll
-                for (int t = 0; t < TN; ++t)
-                    v[m][t] = dot16(a, load16(p.x + min(t, p.T - 1) * p.ldx, (int64_t)c * 16, p.cols, p.x_unit),
-                                    v[m][t]);
-            }
-        }
     }
+    pdl_launch_dependents();
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int t = 0; t < TN; ++t) {
-            v[m][t] = __reduce_add_sync(kFull, v[m][t]);
-            if (lane == 0) sh[warp][m * TN + t] = v[m][t];
-        }
-    if (p.wpr > 1)
-        __syncthreads();
-    else
-        __syncwarp();
-    // lane t of a row's first warp joins token t's sums
-    if (sub == 0 && row < p.rows && lane < p.T) {
-        int r[M];
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // [token][row]
+                red[((warp * M + m) * NB + n) * 128 + (2 * q + (i & 1)) * 16 + g + 8 * (i >> 1)] = acc[m][n][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.T * kFewRows; i += 32 * WARPS) {
+        const int t = i / kFewRows;
+        const int64_t row = row0 + i % kFewRows;
+        if (row >= p.rows) continue;
+        int v[M];
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            r[m] = 0;
-            for (int i = 0; i < p.wpr; ++i) r[m] += sh[warp + i][m * TN + lane];
-            if (p.acc) p.acc[((int64_t)m * p.T + lane) * p.rows + row] = r[m];
+            v[m] = 0;
+            for (int k = 0; k < WARPS; ++k) v[m] += red[(k * M + m) * NB * 128 + i];
+            if (p.acc) p.acc[((int64_t)m * p.T + t) * p.rows + row] = v[m];
         }
-        const float xd = p.xd[lane];
-        float y = (float)r[0] * (xd * p.s[0][row]);
+        const float xd = QUANT ? quant_scale(peak[t]).scale : p.xd[t];
+        float y = (float)v[0] * (xd * p.s[0][row]);
         if constexpr (MODE == kGated)
-            y = act_value(p.act, y) * ((float)r[1] * (xd * p.s[1][row]));
+            y = act_value(p.act, y) * ((float)v[M - 1] * (xd * p.s[M - 1][row]));
         else if (p.bias)
             y += p.bias[row];
-        store_elem(p.out, lane * p.ldo + row, p.dtype, y);
+        store_elem(p.out, t * p.ldo + row, p.dtype, y);
     }
 }
 
@@ -1165,10 +1218,11 @@ static bool tma_operands(const GemmArgs& a) {
     return ok;
 }
 
+// x_type: -1 for codes, else the element type of tokens to quantise.
 template <int MODE>
-static cudaError_t run_dot(const GemmArgs& a, cudaStream_t s) {
-    DotParams p{};
-    bool fast = true;
+static cudaError_t run_few(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s) {
+    FewParams p{};
+    bool fast = a.cols % 16 == 0;
     for (int m = 0; m < a.n_mats; ++m) {
         p.w[m] = a.w[m];
         p.ldw[m] = a.ldw[m];
@@ -1176,10 +1230,10 @@ static cudaError_t run_dot(const GemmArgs& a, cudaStream_t s) {
         p.w_unit[m] = unit_of(a.w[m], a.ldw[m]);
         fast = fast && p.w_unit[m] == 16;
     }
-    p.x = reinterpret_cast<const uint8_t*>(a.x);
+    p.x = x;
     p.ldx = a.ldx;
-    p.x_unit = unit_of(a.x, a.ldx);
-    fast = fast && p.x_unit == 16;
+    p.x_unit = unit_of(x, a.ldx);
+    if (x_type < 0) fast = fast && p.x_unit == 16;
     p.xd = a.xd;
     p.bias = a.bias;
     p.out = a.out;
@@ -1190,29 +1244,51 @@ static cudaError_t run_dot(const GemmArgs& a, cudaStream_t s) {
     p.cols = a.cols;
     p.act = a.act;
     p.dtype = a.dtype;
-    // warps enough for 32 on each SM, while a lane has two chunks or more
-    p.wpr = 1;
-    while (p.wpr < 8 && (int64_t)a.rows * p.wpr < 32 * (int64_t)device_info().sm_count &&
-           a.cols / 16 >= 2 * 32 * 2 * p.wpr)
-        p.wpr *= 2;
-    const int rpc = 8 / p.wpr;
-    const unsigned grid = (unsigned)((a.rows + (int64_t)rpc - 1) / rpc);
-    auto go = [&](auto tn) {
-        constexpr int TN = decltype(tn)::value;
-        if (fast)
-            k_dense_dot<MODE, TN, true><<<grid, kDotThreads, 0, s>>>(p);
-        else
-            k_dense_dot<MODE, TN, false><<<grid, kDotThreads, 0, s>>>(p);
-        return cudaGetLastError();
+    p.dependent = dependent;
+    p.pitch = (a.cols + 127) / 128 * 128 + 64;  // two tokens' 64 bytes fall on different banks
+    const unsigned grid = (unsigned)((a.rows + (int64_t)kFewRows - 1) / kFewRows);
+    auto go = [&](auto nb, auto type, auto is_fast, auto warps) {
+        using XT = decltype(type);
+        constexpr int NB = decltype(nb)::value, WARPS = decltype(warps)::value;
+        auto* kernel = k_dense_few<MODE, NB, XT, decltype(is_fast)::value, WARPS>;
+        static bool attr_done[64];
+        cudaError_t e = allow_smem(kernel, attr_done);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(32 * WARPS);
+        cfg.dynamicSmemBytes = WARPS * (MODE == kGated ? 2 : 1) * NB * 512 + (x_type < 0 ? 0 : 32 * NB + (size_t)a.T * p.pitch);
+        cfg.stream = s;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = dependent ? 1 : 0;
+        return cudaLaunchKernelEx(&cfg, kernel, p);
     };
-    if (a.T == 1) return go(std::integral_constant<int, 1>());
-    if (a.T == 2) return go(std::integral_constant<int, 2>());
-    if (a.T <= 4) return go(std::integral_constant<int, 4>());
-    return go(std::integral_constant<int, 8>());
+    using std::integral_constant;
+    // 16 warps a CTA where the rows give the SMs less than two CTAs each
+    auto by_size = [&](auto type) {
+        auto by_fast = [&](auto is_fast) {
+            auto by_warps = [&](auto nb) {
+                return (int64_t)grid < 2 * (int64_t)device_info().sm_count
+                           ? go(nb, type, is_fast, integral_constant<int, 16>())
+                           : go(nb, type, is_fast, integral_constant<int, 8>());
+            };
+            return a.T <= 8 ? by_warps(integral_constant<int, 1>()) : by_warps(integral_constant<int, 2>());
+        };
+        if constexpr (sizeof(type) > 1)
+            return by_fast(integral_constant<bool, true>());
+        else
+            return fast ? by_fast(integral_constant<bool, true>()) : by_fast(integral_constant<bool, false>());
+    };
+    if (x_type < 0) return by_size(int8_t());
+    if (x_type == MOE_F32) return by_size(float());
+    if (x_type == MOE_BF16) return by_size(__nv_bfloat16());
+    return by_size(__half());
 }
 
-// Tokens up to which the CUDA-core kernel runs, and from which CTA pairs do.
-constexpr int kDotTokens = 4;
+// Pairs from this many tokens on.
 constexpr int kPairTokens = 256;
 
 template <int MODE, int P, typename OT>
@@ -1222,7 +1298,7 @@ static cudaError_t run_product(const GemmArgs& a, cudaStream_t s) {
 
 template <int MODE>
 static cudaError_t run_forward(const GemmArgs& a, cudaStream_t s) {
-    if (a.T <= kDotTokens) return run_dot<MODE>(a, s);
+    if (a.T <= kFewTokens) return run_few<MODE>(a, a.x, -1, false, s);
     return a.dtype == MOE_F32    ? run_product<MODE, 1, float>(a, s)
            : a.dtype == MOE_BF16 ? run_product<MODE, 1, __nv_bfloat16>(a, s)
                                  : run_product<MODE, 1, __half>(a, s);
@@ -1231,6 +1307,21 @@ static cudaError_t run_forward(const GemmArgs& a, cudaStream_t s) {
 cudaError_t launch_matmul(const GemmArgs& a, cudaStream_t s) { return run_forward<kMatmul>(a, s); }
 
 cudaError_t launch_gated(const GemmArgs& a, cudaStream_t s) { return run_forward<kGated>(a, s); }
+
+bool few_quantised_fits(const GemmArgs& a, const void* x, int x_type) {
+    bool ok = a.T <= kFewTokens && a.cols % 16 == 0 && (int64_t)a.T * a.cols <= 96 * 1024 &&
+              unit_of(x, a.ldx * (x_type == MOE_F32 ? 4 : 2)) == 16;
+    for (int m = 0; m < a.n_mats; ++m) ok = ok && unit_of(a.w[m], a.ldw[m]) == 16;
+    return ok;
+}
+
+cudaError_t launch_matmul_quantised(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s) {
+    return run_few<kMatmul>(a, x, x_type, dependent, s);
+}
+
+cudaError_t launch_gated_quantised(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s) {
+    return run_few<kGated>(a, x, x_type, dependent, s);
+}
 
 cudaError_t launch_grad_matmul(const GemmArgs& a, cudaStream_t s) {
     return a.dtype == MOE_F32    ? run_product<kGrad, planes_of(MOE_F32), float>(a, s)

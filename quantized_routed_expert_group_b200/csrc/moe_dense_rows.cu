@@ -9,8 +9,6 @@
 namespace moe {
 namespace dense {
 
-constexpr uint32_t kInfBits = 0x7F800000u;
-
 // The largest |v| of a CTA, as bits: as integers, magnitudes order as the
 // numbers do, and infinities and NaNs come above every finite value (a
 // floating maximum would drop a NaN).  `buf` alternates between calls, so one
@@ -23,78 +21,13 @@ __device__ __forceinline__ uint32_t block_max_bits(uint32_t m, uint32_t* sh, int
     return __reduce_max_sync(kFull, lane < nw ? sh[buf * 32 + lane] : 0u);
 }
 
-// VEC consecutive elements of a row, in 16- or 8-byte loads (the caller checked the alignment).
-template <typename T, int VEC>
-struct Raw {
-    static constexpr int kWords = VEC * (int)sizeof(T) / 4;
-    union {
-        T e[VEC];
-        uint32_t w[kWords > 0 ? kWords : 1];
-    };
-    __device__ __forceinline__ Raw() {}
-    __device__ __forceinline__ void load(const T* p) {
-        if constexpr (VEC == 1) {
-            e[0] = *p;
-        } else if constexpr (kWords == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(p);
-            w[0] = v.x;
-            w[1] = v.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-                w[4 * i] = v.x;
-                w[4 * i + 1] = v.y;
-                w[4 * i + 2] = v.z;
-                w[4 * i + 3] = v.w;
-            }
-        }
-    }
-    __device__ __forceinline__ T get(int i) const { return e[i]; }
-};
-
-// Byte K of four words, in order.
-template <int K>
-__device__ __forceinline__ uint32_t gather_byte(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    const uint32_t ab = __byte_perm(a, b, K | ((K + 4) << 4));
-    const uint32_t cd = __byte_perm(c, d, K | ((K + 4) << 4));
-    return __byte_perm(ab, cd, 0x5410);
-}
-
-// Byte K of VEC words, XOR-ed with flip, as codes in one store.
-template <int VEC, int K>
-__device__ __forceinline__ void store_bytes(int8_t* p, const int (&c)[VEC], uint32_t flip) {
-    if constexpr (VEC == 1) {
-        *p = (int8_t)(((uint32_t)c[0] >> (8 * K)) ^ (flip & 0xFFu));
-    } else {
-        uint32_t w[VEC / 4];
-#pragma unroll
-        for (int i = 0; i < VEC / 4; ++i)
-            w[i] = gather_byte<K>((uint32_t)c[4 * i], (uint32_t)c[4 * i + 1], (uint32_t)c[4 * i + 2],
-                                  (uint32_t)c[4 * i + 3]) ^ flip;
-        if constexpr (VEC == 4)
-            *reinterpret_cast<uint32_t*>(p) = w[0];
-        else
-            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    }
-}
-
 // ---------------------------------------------------------------------------
 // Per-token quantiser: one CTA a row.  d = amax / 127, q = round-half-away(x *
-// (1/d)), the steps of the block quantiser over the whole row.  Rows below
-// 2^-112 store zeros (so d is a normal number and 1/d finite); a row with an
-// infinity or a NaN stores d = NaN, so that whatever is computed from it says so.
+// (1/d)), the steps of the block quantiser over the whole row.
 // Memory bound: the row is read once and kept in registers (rows up to
-// kCache * VEC * blockDim elements; longer ones are read again from L2).
+// kQuantCache * VEC * blockDim elements; longer ones are read again from L2).
 // ---------------------------------------------------------------------------
-constexpr int kQuantCache = 4;
-constexpr float kTinyRow = 1.925929944387236e-34f;  // 2^-112
-
-// round-half-away-from-zero of |v| < 2^23: adding half towards zero never
-// carries past an integer that v + half does not reach, and the conversion cuts
-// the rest.  (127 fl(1/d) d stays below 127.5, so no clamp is needed; 0 * inf
-// and NaN convert to 0.)
-__device__ __forceinline__ int round_away(float v) { return __float2int_rz(__fadd_rz(v, copysignf(0.5f, v))); }
+constexpr int kQuantCache = 8;
 
 template <int DT, int VEC>
 __global__ void __launch_bounds__(512)
@@ -126,11 +59,9 @@ __global__ void __launch_bounds__(512)
         peak(e);
     }
     m = block_max_bits(m, sh, 0);
-    const float amax = __uint_as_float(m);
-    const bool live = m < kInfBits && amax >= kTinyRow;
-    const float scale = live ? __fdiv_rn(amax, 127.0f) : 0.0f;
-    const float inv = live ? __fdiv_rn(1.0f, scale) : 0.0f;
-    if (threadIdx.x == 0) d[row] = m >= kInfBits ? __uint_as_float(0x7FC00000u) : scale;
+    const QuantScale qs = quant_scale(m);
+    const float inv = qs.inv;
+    if (threadIdx.x == 0) d[row] = qs.scale;
     auto put = [&](const Raw<T, VEC>& r, int c) {
         int o[VEC];
 #pragma unroll
@@ -157,7 +88,11 @@ static cudaError_t quantize_token(const void* x, int64_t rows, int cols, int64_t
     const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx % kVec == 0 && cols % kVec == 0 &&
                      reinterpret_cast<uintptr_t>(q) % kVec == 0 && ldq % kVec == 0;
     const int per = vec ? kVec : 1;
-    int threads = ((cols + per - 1) / per + 31) / 32 * 32;
+    // many rows: small CTAs with several loads a thread in flight, so that all
+    // rows of an SM are under way together; few rows: as wide as the row
+    const int groups = (cols + per - 1) / per;
+    const int each = rows >= 2 * device_info().sm_count ? 6 : 1;
+    int threads = (groups + 32 * each - 1) / (32 * each) * 32;
     threads = threads > 512 ? 512 : threads;
     for (int64_t r = 0; r < rows; r += 1 << 30) {  // the grid's limit
         const unsigned grid = (unsigned)(rows - r < (1 << 30) ? rows - r : (1 << 30));

@@ -107,3 +107,39 @@ def test_gated_backward(T, K, N, act, dtype):
     for name, g, (want, tol) in zip(("dx", "ds_gate", "ds_up"), got, refs):
         dh.check(name, g, want, tol)
     assert moe.dense_device_error() == 0
+
+
+def bank_of(ws, ss):
+    g, u, d = (w.view(torch.uint8).cuda()[None] for w in ws)
+    sg, su, sd = (s.cuda()[None] for s in ss)
+    return moe.ExpertBank(g, u, d, sg, su, sd)
+
+
+def ffn_inputs(T, H, I, dtype):
+    gen = torch.Generator().manual_seed(T + H + I)
+    x = torch.randn((T, H), generator=gen).to(DT[dtype])
+    ws = [dh.codes(gen, r, c) for r, c in ((I, H), (I, H), (H, I))]
+    ss = [(torch.rand(r, generator=gen) + 0.5) / (50.0 * c ** 0.5) for r, c in ((I, H), (I, H), (H, I))]
+    return x, ws, ss
+
+
+# (300, ..) and up run the tiled kernels, 5 to 16 the weight stream with tokens quantised inside, and
+# 1000 x 500 and 36 x 20 rows off the 16-byte grid
+FFN = [(1, 256, 128), (1, 6144, 2048), (3, 512, 96), (4, 6144, 2048), (5, 1000, 500), (8, 1024, 304), (9, 1024, 304),
+       (16, 2048, 640), (17, 512, 256), (2, 36, 20), (300, 1024, 512), (130, 264, 72)]
+
+
+@pytest.mark.parametrize("T,H,I", FFN)
+@pytest.mark.parametrize("act,dtype", [("silu", "bf16"), ("gelu", "fp32"), ("silu", "fp16")])
+def test_dense_ffn_is_its_steps(T, H, I, act, dtype):
+    """The run of the operators equals them called one by one, bit for bit."""
+    x, ws, ss = ffn_inputs(T, H, I, dtype)
+    bank = bank_of(ws, ss)
+    xc = x.cuda()
+    got = moe.dense_ffn(xc, bank, act=act)
+    q, d = moe.quantize_act_token(xc)
+    h = moe.gated_ffn(q, d, bank.w_gate[0], bank.s_gate[0], bank.w_up[0], bank.s_up[0], act=act)
+    hq, hd = moe.quantize_act_token(h)
+    want = moe.int8_matmul(hq, hd, bank.w_down[0], bank.s_down[0], out_dtype=DT[dtype])
+    assert torch.equal(got, want)
+    assert moe.dense_device_error() == 0
