@@ -490,33 +490,70 @@ __global__ void __launch_bounds__(32 * WARPS) k_dense_few(const FewParams p) {
     };
     load_w(warp);
     if constexpr (QUANT) {
-        if (p.dependent) pdl_wait();
         if (threadIdx.x < 8 * NB) peak[threadIdx.x] = 0;
         __syncthreads();
-        constexpr int V = 16 / (int)sizeof(XT);
+        if (p.dependent) pdl_wait();
+        // `per` warps a token (one warp takes every WARPS-th token where there are
+        // more): its vectors loaded together and kept for the second pass
+        constexpr int V = 16 / (int)sizeof(XT), kKeep = 8;
+        const int per = max(1, WARPS / p.T), sub = warp % per;
         const XT* x = static_cast<const XT*>(p.x);
-        for (int t = 0; t < p.T; ++t) {
+        Raw<XT, V> e[kKeep];
+        const int c0 = V * (lane + 32 * sub), step = V * 32 * per;
+        auto peak_of = [&](const Raw<XT, V>& r, uint32_t m) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(to_f32(r.get(i))) & 0x7FFFFFFFu);
+            return m;
+        };
+        auto scan = [&](int t) {
+            const XT* xr = x + t * p.ldx;
             uint32_t m = 0;
-            for (int c = V * threadIdx.x; c < p.cols; c += 32 * V * WARPS) {
-                Raw<XT, V> e;
-                e.load(x + t * p.ldx + c);
 #pragma unroll
-                for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(to_f32(e.get(i))) & 0x7FFFFFFFu);
-            }
-            m = __reduce_max_sync(kFull, m);
-            if (lane == 0) atomicMax(&peak[t], m);
-        }
-        __syncthreads();
-        for (int t = 0; t < p.T; ++t) {
-            const float inv = quant_scale(peak[t]).inv;
-            for (int c = V * threadIdx.x; c < p.cols; c += 32 * V * WARPS) {
-                Raw<XT, V> e;
-                int o[V];
-                e.load(x + t * p.ldx + c);
+            for (int i = 0; i < kKeep; ++i)
+                if (c0 + i * step < p.cols) e[i].load(xr + c0 + i * step);
 #pragma unroll
-                for (int i = 0; i < V; ++i) o[i] = round_away(__fmul_rn(to_f32(e.get(i)), inv));
-                store_bytes<V, 0>(reinterpret_cast<int8_t*>(codes) + t * p.pitch + c, o, 0u);
+            for (int i = 0; i < kKeep; ++i)
+                if (c0 + i * step < p.cols) m = peak_of(e[i], m);
+            for (int c = c0 + kKeep * step; c < p.cols; c += step) {
+                Raw<XT, V> r;
+                r.load(xr + c);
+                m = peak_of(r, m);
             }
+            return __reduce_max_sync(kFull, m);
+        };
+        auto put = [&](int t, uint32_t m) {
+            const XT* xr = x + t * p.ldx;
+            int8_t* o = reinterpret_cast<int8_t*>(codes) + t * p.pitch;
+            const float inv = quant_scale(m).inv;
+            auto one = [&](const Raw<XT, V>& r, int c) {
+                int q8[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) q8[i] = round_away(__fmul_rn(to_f32(r.get(i)), inv));
+                store_bytes<V, 0>(o + c, q8, 0u);
+            };
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i)
+                if (c0 + i * step < p.cols) one(e[i], c0 + i * step);
+            for (int c = c0 + kKeep * step; c < p.cols; c += step) {
+                Raw<XT, V> r;
+                r.load(xr + c);
+                one(r, c);
+            }
+        };
+        if (per == 1) {
+            for (int t = warp; t < p.T; t += WARPS) {
+                const uint32_t m = scan(t);
+                if (lane == 0) peak[t] = m;
+                put(t, m);
+            }
+        } else {
+            const int t = warp / per;
+            if (t < p.T) {
+                const uint32_t m = scan(t);
+                if (lane == 0) atomicMax(&peak[t], m);
+            }
+            __syncthreads();
+            if (t < p.T) put(t, peak[t]);
         }
         __syncthreads();
     }

@@ -414,28 +414,23 @@ def _addr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-class _On:
-    """The call's device and stream as the current ones, so that its
-    allocations belong to the stream that uses them; gives the stream's handle."""
-    __slots__ = ("dev", "contexts")
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-    def __init__(self, dev: int, stream):
-        self.dev, self.contexts = dev, ()
-        if stream is not None:
-            if stream.device.index != dev:
-                raise ValueError(f"stream is on {stream.device}, the call's tensors on cuda:{dev}")
-            self.contexts = (torch.cuda.stream(stream),)  # also makes its device the current one
-        elif dev != torch.cuda.current_device():
-            self.contexts = (torch.cuda.device(dev),)
 
-    def __enter__(self) -> int:
-        for c in self.contexts:
-            c.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.dev)
-
-    def __exit__(self, *exc):
-        for c in self.contexts:
-            c.__exit__(*exc)
+def _on(dev: int, stream, call):
+    """call(stream handle) with the call's device and stream as the current ones,
+    so that what it allocates belongs to the stream that uses it."""
+    if stream is None:
+        if dev == _current_device():
+            return call(_raw_stream(dev))
+        with torch.cuda.device(dev):
+            return call(_raw_stream(dev))
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, the call's tensors on cuda:{dev}")
+    with torch.cuda.stream(stream):  # also makes its device the current one
+        return call(stream.cuda_stream)
 
 
 def quantize_act_token(x: torch.Tensor, stream=None):
@@ -443,17 +438,20 @@ def quantize_act_token(x: torch.Tensor, stream=None):
     fp32 (see moe_quantize_act_token)."""
     ld = _matrix(x, _ROW_TYPES, "x")
     T, K = x.shape
-    with _On(x.get_device(), stream) as s:
-        q = torch.empty((T, K), dtype=torch.int8, device=x.device)
+
+    def call(s):
+        q = torch.empty(T, K, dtype=torch.int8, device=x.device)
         d = torch.empty(T, dtype=torch.float32, device=x.device)
         _check(lib().moe_quantize_act_token(x.data_ptr(), _DTYPES[x.dtype], T, K, ld, q.data_ptr(), K, d.data_ptr(),
                                             s), "quantize_act_token")
-    return q, d
+        return q, d
+
+    return _on(x.get_device(), stream, call)
 
 
 def _result(out, T, N, dtype, like, dev):
     if out is None:
-        return torch.empty((T, N), dtype=dtype, device=like.device), N
+        return torch.empty(T, N, dtype=dtype, device=like.device), N
     return out, _matrix(out, (dtype,), "out", T, N, dev)
 
 
@@ -472,12 +470,15 @@ def int8_matmul(xq: torch.Tensor, xd: torch.Tensor, w: torch.Tensor, s: torch.Te
     if bias is not None:
         _vector(bias, N, "bias", dev)
     dt = _choice(out_dtype, _DTYPES, "out_dtype")
-    with _On(dev, stream) as st:
+
+    def call(st):
         y, ldo = _result(out, T, N, out_dtype, xq, dev)
-        acc = torch.empty((T, N), dtype=torch.int32, device=xq.device) if save else None
+        acc = torch.empty(T, N, dtype=torch.int32, device=xq.device) if save else None
         _check(lib().moe_int8_matmul(xq.data_ptr(), ldx, xd.data_ptr(), T, w.data_ptr(), ldw, s.data_ptr(), N, K,
                                      _addr(bias), y.data_ptr(), dt, ldo, _addr(acc), st), "int8_matmul")
-    return (y, acc) if save else y
+        return (y, acc) if save else y
+
+    return _on(dev, stream, call)
 
 
 def int8_matmul_backward(dy: torch.Tensor, acc: torch.Tensor | None, xd: torch.Tensor | None, w: torch.Tensor,
@@ -496,8 +497,9 @@ def int8_matmul_backward(dy: torch.Tensor, acc: torch.Tensor | None, xd: torch.T
     else:
         xd = None
     dt = _DTYPES[dy.dtype]
-    with _On(dev, stream) as st:
-        dx = torch.empty((T, K), dtype=dy.dtype, device=dy.device)
+
+    def call(st):
+        dx = torch.empty(T, K, dtype=dy.dtype, device=dy.device)
         ds = torch.empty(N, dtype=torch.float32, device=dy.device) if acc is not None else None
         db = torch.empty(N, dtype=torch.float32, device=dy.device) if bias_grad else None
         size = lib().moe_int8_backward_workspace_bytes(1, T, N, dt)
@@ -505,7 +507,9 @@ def int8_matmul_backward(dy: torch.Tensor, acc: torch.Tensor | None, xd: torch.T
         _check(lib().moe_int8_matmul_backward(dy.data_ptr(), dt, lddy, _addr(acc), _addr(xd), T, w.data_ptr(), ldw,
                                               s.data_ptr(), N, K, dx.data_ptr(), K, _addr(ds), _addr(db),
                                               ws.data_ptr(), size, st), "int8_matmul_backward")
-    return dx, ds, db
+        return dx, ds, db
+
+    return _on(dev, stream, call)
 
 
 def gated_ffn(xq: torch.Tensor, xd: torch.Tensor, w_gate: torch.Tensor, s_gate: torch.Tensor, w_up: torch.Tensor,
@@ -524,13 +528,16 @@ def gated_ffn(xq: torch.Tensor, xd: torch.Tensor, w_gate: torch.Tensor, s_gate: 
     _vector(s_gate, N, "s_gate", dev)
     _vector(s_up, N, "s_up", dev)
     dt, ac = _choice(out_dtype, _DTYPES, "out_dtype"), _choice(act, _ACTS, "act")
-    with _On(dev, stream) as st:
+
+    def call(st):
         h, ldo = _result(out, T, N, out_dtype, xq, dev)
-        acc = torch.empty((2, T, N), dtype=torch.int32, device=xq.device) if save else None
+        acc = torch.empty(2, T, N, dtype=torch.int32, device=xq.device) if save else None
         _check(lib().moe_gated_ffn(xq.data_ptr(), ldx, xd.data_ptr(), T, w_gate.data_ptr(), ldg, s_gate.data_ptr(),
                                    w_up.data_ptr(), ldu, s_up.data_ptr(), N, K, ac, h.data_ptr(), dt, ldo, _addr(acc),
                                    st), "gated_ffn")
-    return (h, acc) if save else h
+        return (h, acc) if save else h
+
+    return _on(dev, stream, call)
 
 
 def gated_ffn_backward(dh: torch.Tensor, acc: torch.Tensor, xd: torch.Tensor, w_gate: torch.Tensor,
@@ -549,9 +556,10 @@ def gated_ffn_backward(dh: torch.Tensor, acc: torch.Tensor, xd: torch.Tensor, w_
     _vector(s_gate, N, "s_gate", dev)
     _vector(s_up, N, "s_up", dev)
     dt, ac = _DTYPES[dh.dtype], _choice(act, _ACTS, "act")
-    with _On(dev, stream) as st:
-        dx = torch.empty((T, K), dtype=dh.dtype, device=dh.device)
-        ds = torch.empty((2, N), dtype=torch.float32, device=dh.device)
+
+    def call(st):
+        dx = torch.empty(T, K, dtype=dh.dtype, device=dh.device)
+        ds = torch.empty(2, N, dtype=torch.float32, device=dh.device)
         size = lib().moe_int8_backward_workspace_bytes(2, T, N, dt)
         ws = torch.empty(size, dtype=torch.uint8, device=dh.device)
         dsg, dsu = ds.unbind()
@@ -559,7 +567,9 @@ def gated_ffn_backward(dh: torch.Tensor, acc: torch.Tensor, xd: torch.Tensor, w_
                                             w_gate.data_ptr(), ldg, s_gate.data_ptr(), w_up.data_ptr(), ldu,
                                             s_up.data_ptr(), N, K, ac, dx.data_ptr(), K, dsg.data_ptr(),
                                             dsu.data_ptr(), ws.data_ptr(), size, st), "gated_ffn_backward")
-    return dx, dsg, dsu
+        return dx, dsg, dsu
+
+    return _on(dev, stream, call)
 
 
 def dense_ffn(x: torch.Tensor, bank: ExpertBank, act: str = "silu", out: torch.Tensor | None = None,
@@ -579,13 +589,16 @@ def dense_ffn(x: torch.Tensor, bank: ExpertBank, act: str = "silu", out: torch.T
         if t.dtype != want or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
             raise ValueError(f"bank.{name} must be a contiguous {want} tensor {shape} on cuda:{dev} (one int8 expert)")
     dt, ac = _DTYPES[x.dtype], _choice(act, _ACTS, "act")
-    with _On(dev, stream) as st:
+
+    def call(st):
         y, ldo = _result(out, T, H, x.dtype, x, dev)
         size = lib().moe_dense_ffn_workspace_bytes(T, H, I)
         ws = torch.empty(size, dtype=torch.uint8, device=x.device)
         _check(lib().moe_dense_ffn(x.data_ptr(), dt, ldx, T, H, I, ctypes.byref(bank.struct()), ac, y.data_ptr(), ldo,
                                    ws.data_ptr(), size, st), "dense_ffn")
-    return y
+        return y
+
+    return _on(dev, stream, call)
 
 
 def dense_device_error(stream=None) -> int:
