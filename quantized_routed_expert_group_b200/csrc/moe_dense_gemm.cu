@@ -101,15 +101,90 @@ __device__ __forceinline__ uint4 load16(const uint8_t* row, int64_t c, int64_t c
     return u.v;
 }
 
+// Asynchronous copy of up to BYTES bytes (n of them; the rest is zero-filled).
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int n) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n)
+                     : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// At most `ahead` (0, 1 or 2) of this thread's groups still on their way.
+__device__ __forceinline__ void cp_async_wait(int ahead) {
+    if (ahead == 0)
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (ahead == 1)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
+
+template <int UNIT>
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* row, int64_t c, int left) {
+#pragma unroll
+    for (int i = 0; i < 16; i += UNIT) {
+        const int n = min(max(left - i, 0), UNIT);
+        cp_async<UNIT>(dst + i, n > 0 ? row + c + i : row, n);
+    }
+}
+
 // A tile of n rows of 128 bytes at (row0, col0) of [rows][cols] into the
-// 128-byte-swizzle layout, by 128 threads.
+// 128-byte-swizzle layout, by 128 threads (16 rows a pass); bytes outside read
+// as zero.  Rows on a 16-, 8- or 4-byte grid are copied asynchronously (the
+// caller commits and waits); others are put together from aligned words, four
+// passes of loads under way at a time.
 __device__ __forceinline__ void load_tile_direct(uint8_t* tile, const uint8_t* base, int64_t ld, int64_t rows,
                                                  int64_t cols, int64_t row0, int64_t col0, int n, int unit, int tid) {
     const int c = tid & 7;
-    for (int r = tid >> 3; r < n; r += 16) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row0 + r < rows) v = load16(base + (row0 + r) * ld, col0 + 16 * c, cols, unit);
-        *reinterpret_cast<uint4*>(tile + sw128_chunk(r, c)) = v;
+    const int64_t col = col0 + 16 * c;
+    const int in_row = (int)min((int64_t)16, max((int64_t)0, cols - col));  // bytes of the chunk inside the row
+    if (unit >= 4) {
+        for (int r = tid >> 3; r < n; r += 16) {
+            const bool ok = row0 + r < rows;
+            const uint8_t* row = base + (ok ? row0 + r : 0) * ld;
+            const uint32_t dst = smem_addr(tile + sw128_chunk(r, c));
+            const int left = ok ? in_row : 0;
+            if (unit == 16)
+                copy16<16>(dst, row, col, left);
+            else if (unit == 8)
+                copy16<8>(dst, row, col, left);
+            else
+                copy16<4>(dst, row, col, left);
+        }
+        return;
+    }
+    for (int r0 = tid >> 3; r0 < n; r0 += 64) {
+        uint32_t w[4][5];
+        int shift[4], left[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = r0 + 16 * k;
+            const bool ok = r < n && row0 + r < rows;
+            const uint8_t* src = base + (ok ? row0 + r : 0) * ld + col;
+            shift[k] = 8 * (int)(reinterpret_cast<uintptr_t>(src) & 3);
+            left[k] = ok ? in_row : 0;
+            // the aligned words that hold the chunk's bytes inside the row
+            const uint32_t* ws = reinterpret_cast<const uint32_t*>(src - shift[k] / 8);
+            const int words = left[k] ? (shift[k] / 8 + left[k] + 3) / 4 : 0;
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[k][i] = i < words ? __ldg(ws + i) : 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = r0 + 16 * k;
+            if (r >= n) break;
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[i] = __funnelshift_r(w[k][i], w[k][i + 1], shift[k]);
+                const int keep = left[k] - 4 * i;  // bytes of this word inside the row
+                o[i] = keep >= 4 ? o[i] : keep <= 0 ? 0u : o[i] & ((1u << (8 * keep)) - 1u);
+            }
+            *reinterpret_cast<uint4*>(tile + sw128_chunk(r, c)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
     }
 }
 
@@ -317,36 +392,43 @@ __global__ void __launch_bounds__(kTileThreads)
         }
         __syncwarp();
     } else if (p.direct) {
-        // ---------------- plain loads (operands off the 16-byte grid) ----------------
-        const int tid = threadIdx.x - 64;
-        int s = 0;
-        uint32_t ph = 0;
-        for (int ks = ks0; ks < ks1; ++ks) {
-            if (!mbar_wait_ns(&empty[s], ph ^ 1u, kWaitNs)) {
-                set_error(&g_dense_error, kErrTimeout);
-                break;
+        // ---------------- operands off the 16-byte grid ----------------
+        // Stage it's copies are left on their way while the next `ahead` are
+        // issued; then they are waited for, made visible to the tensor core
+        // and announced.
+        const int tid = threadIdx.x - 64, n_st = ks1 - ks0;
+        const int ahead = min(2, p.stages - 1);
+        for (int it = 0; it < n_st + ahead; ++it) {
+            if (it < n_st) {
+                const int ks = ks0 + it, s = it % p.stages;
+                if (!mbar_wait_ns(&empty[s], ((uint32_t)(it / p.stages) & 1u) ^ 1u, kWaitNs)) {
+                    set_error(&g_dense_error, kErrTimeout);
+                    break;
+                }
+                uint8_t* st = sm + s * p.stage_bytes;
+                if constexpr (MODE == kGrad) {
+                    const int m = ks / p.k_steps, k = (ks - m * p.k_steps) * kStageK;
+                    load_tile_direct(st, p.w[m], p.ldw[m], p.rows, p.cols, k, n0, kTileRows, p.w_unit[m], tid);
+                    for (int i = 0; i < P; ++i)
+                        load_tile_direct(st + kATile + i * p.nt * kStageK,
+                                         p.x + (int64_t)i * p.T * p.ldx + m * p.mat_pitch, p.ldx, p.T, p.rows, t0, k,
+                                         p.nt, p.x_unit, tid);
+                } else {
+                    for (int m = 0; m < kA; ++m)
+                        load_tile_direct(st + m * kATile, p.w[m], p.ldw[m], p.rows, p.cols, n0, (int64_t)ks * kStageK,
+                                         kTileRows, p.w_unit[m], tid);
+                    load_tile_direct(st + kA * kATile, p.x, p.ldx, p.T, p.cols, t0, (int64_t)ks * kStageK, p.nt,
+                                     p.x_unit, tid);
+                }
             }
-            uint8_t* st = sm + s * p.stage_bytes;
-            if constexpr (MODE == kGrad) {
-                const int m = ks / p.k_steps, k = (ks - m * p.k_steps) * kStageK;
-                load_tile_direct(st, p.w[m], p.ldw[m], p.rows, p.cols, k, n0, kTileRows, p.w_unit[m], tid);
-                for (int i = 0; i < P; ++i)
-                    load_tile_direct(st + kATile + i * p.nt * kStageK, p.x + (int64_t)i * p.T * p.ldx + m * p.mat_pitch,
-                                     p.ldx, p.T, p.rows, t0, k, p.nt, p.x_unit, tid);
-            } else {
-                for (int m = 0; m < kA; ++m)
-                    load_tile_direct(st + m * kATile, p.w[m], p.ldw[m], p.rows, p.cols, n0, (int64_t)ks * kStageK,
-                                     kTileRows, p.w_unit[m], tid);
-                load_tile_direct(st + kA * kATile, p.x, p.ldx, p.T, p.cols, t0, (int64_t)ks * kStageK, p.nt, p.x_unit,
-                                 tid);
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&full[s]);
-            if (++s == p.stages) {
-                s = 0;
-                ph ^= 1u;
+            cp_async_commit();  // (an empty group after the last stage)
+            if (it >= ahead) {
+                cp_async_wait(ahead);
+                fence_proxy_async_smem();
+                mbar_arrive(&full[(it - ahead) % p.stages]);
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
     }
 

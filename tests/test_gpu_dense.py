@@ -143,3 +143,51 @@ def test_dense_ffn_is_its_steps(T, H, I, act, dtype):
     want = moe.int8_matmul(hq, hd, bank.w_down[0], bank.s_down[0], out_dtype=DT[dtype])
     assert torch.equal(got, want)
     assert moe.dense_device_error() == 0
+
+
+def strided(t, offset, pitch, fill=None):
+    """t as a view of a larger buffer: `offset` elements into it, rows `pitch` elements apart."""
+    rows, cols = t.shape
+    buf = torch.full((offset + rows * pitch + 64,), 77 if fill is None else fill, dtype=t.dtype, device="cuda")
+    v = buf[offset:offset + rows * pitch].view(rows, pitch)[:, :cols]
+    v.copy_(t)
+    return buf, v
+
+
+# every loader (16, 8, 4 bytes and single ones), each with short and long batches; row strides beyond the row
+@pytest.mark.parametrize("T", [3, 40, 300])
+@pytest.mark.parametrize("offset,extra", [(0, 16), (16, 32), (8, 8), (4, 12), (1, 3), (3, 0), (2, 6)])
+def test_strided_operands_and_results(T, offset, extra):
+    K, N, dtype = 272, 136, torch.bfloat16
+    x, xd, ws, ss, bias, dy = dh.inputs(T + offset, T, K, N, 2, dtype)
+    cd = cuda(xd, ss[0], ss[1], bias)
+    _, xv = strided(x, offset, K + extra)
+    wv = [strided(w, offset, K + extra)[1] for w in ws]
+    obuf, ov = strided(torch.zeros((T, N), dtype=dtype), offset, N + extra)
+    acc, y, tol = dh.ref_matmul(x, xd, ws[0], ss[0], bias, dtype)
+    got = moe.int8_matmul(xv, cd[0], wv[0], cd[1], bias=cd[3], out_dtype=dtype, out=ov)
+    assert got is ov
+    dh.check("y", ov, y, tol)
+    padded = obuf[offset:offset + T * (N + extra)].view(T, N + extra)[:, N:]
+    assert (padded == 77).all() and (obuf[:offset] == 77).all() and (obuf[offset + T * (N + extra):] == 77).all()
+    sums, h, tol = dh.ref_gated(x, xd, ws, ss, "silu", dtype)
+    obuf, ov = strided(torch.zeros((T, N), dtype=dtype), offset, N + extra)
+    _, got_acc = moe.gated_ffn(xv, cd[0], wv[0], cd[1], wv[1], cd[2], out_dtype=dtype, out=ov, save=True)
+    dh.check("h", ov, h, tol)
+    assert torch.equal(got_acc.cpu().double(), sums)
+    padded = obuf[offset:offset + T * (N + extra)].view(T, N + extra)[:, N:]
+    assert (padded == 77).all() and (obuf[:offset] == 77).all()
+    _, dyv = strided(dy, offset, N + extra)
+    for name, g, (want, tol) in zip(("dx", "ds_gate", "ds_up"),
+                                    moe.gated_ffn_backward(dyv, got_acc, cd[0], wv[0], cd[1], wv[1], cd[2]),
+                                    dh.ref_gated_backward(dy, sums, xd, ws, ss, "silu", dtype)):
+        dh.check(name, g, want, tol)
+    for name, g, (want, tol) in zip(("dx", "ds", "dbias"),
+                                    moe.int8_matmul_backward(dyv, got_acc[0].contiguous(), cd[0], wv[0], cd[1], True),
+                                    dh.ref_matmul_backward(dy, sums[0], xd, ws[0], ss[0], dtype)):
+        dh.check(name, g, want, tol)
+    xf = torch.randn((T, K)).to(dtype)
+    _, xfv = strided(xf, offset, K + extra)
+    (q, d), (q0, d0) = moe.quantize_act_token(xfv), moe.quantize_act_token(xf.cuda())
+    assert torch.equal(q, q0) and torch.equal(d, d0)
+    assert moe.dense_device_error() == 0
