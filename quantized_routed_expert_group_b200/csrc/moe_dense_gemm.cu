@@ -59,7 +59,8 @@ struct TileParams {
     int stage_bytes;
     int tmem_cols;
     int act, dtype;
-    int direct;     // operands that TMA cannot take: plain loads by the epilogue warps
+    int quad;       // results and sums may be stored four at a time
+    int direct;     // operands that TMA cannot take: loads by the epilogue warps
     int w_unit[kMaxMats], x_unit;  // direct: bytes of the widest aligned load
 };
 
@@ -193,12 +194,22 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ int ld_peer(const int32_t* p, uint32_t rank) {
+// Four sums of the CTA `rank` of the cluster, at this CTA's address p.
+__device__ __forceinline__ int4 ld_peer(const int32_t* p, uint32_t rank) {
     uint32_t a;
-    int v;
+    int4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
     return v;
+}
+
+// TMEM words as the integers they are.
+template <int N>
+__device__ __forceinline__ uint32_t (&as_words(int (&v)[N]))[N] {
+    return reinterpret_cast<uint32_t(&)[N]>(v);
 }
 
 // Where a product's results go, for lanes that are channels.
@@ -211,33 +222,37 @@ struct ChannelOut {
     int act;
 };
 
+// A result from its integer sums v[.][j] (gated: gate and up; gradient: the
+// planes) and scales: the token's, the channel's, the bias.
+template <int MODE, int P, int N>
+__device__ __forceinline__ float join(const int (&v)[MODE == kGated ? 2 : P][N], int j, const RowScale tok, float s0,
+                                      float s1, float bias, int act) {
+    if constexpr (MODE == kGrad) {
+        // digits joined in fp32: each plane's sum rounds by 2^-24 of itself
+        float d = (float)v[P - 1][j];
+#pragma unroll
+        for (int i = P - 2; i >= 0; --i) d = fmaf(d, 256.0f, (float)v[i][j]);
+        return d * tok.a * tok.b;
+    } else if constexpr (MODE == kGated) {
+        return act_value(act, (float)v[0][j] * (tok.a * s0)) * ((float)v[1][j] * (tok.a * s1));
+    } else {
+        return (float)v[0][j] * (tok.a * s0) + bias;
+    }
+}
+
 // The results of one channel n for up to N consecutive tokens t ..: `v` are the
 // integer sums (gated: gate and up; gradient: planes), `ts` the tokens' scales
 // (16-byte aligned).  All values are formed before the first store, so that the
 // columns' arithmetic overlaps; a warp's stores run along the tokens' rows.
 template <int MODE, int P, typename OT, int N>
-__device__ __forceinline__ void emit_channel(const ChannelOut& o, const uint32_t (&v)[MODE == kGated ? 2 : P][N],
-                                             int64_t t, int n, int valid, const RowScale* ts, float s0, float s1,
-                                             float bias) {
+__device__ __forceinline__ void emit_channel(const ChannelOut& o, const int (&v)[MODE == kGated ? 2 : P][N], int64_t t,
+                                             int n, int valid, const RowScale* ts, float s0, float s1, float bias) {
     float f[N];
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
         const float4 sc = *reinterpret_cast<const float4*>(ts + j);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float a = k ? sc.z : sc.x, b = k ? sc.w : sc.y;
-            if constexpr (MODE == kGrad) {
-                // digits joined in fp32: each plane's sum rounds by 2^-24 of itself
-                float d = (float)(int)v[P - 1][j + k];
-#pragma unroll
-                for (int i = P - 2; i >= 0; --i) d = fmaf(d, 256.0f, (float)(int)v[i][j + k]);
-                f[j + k] = d * a * b;
-            } else if constexpr (MODE == kGated) {
-                f[j + k] = act_value(o.act, (float)(int)v[0][j + k] * (a * s0)) * ((float)(int)v[1][j + k] * (a * s1));
-            } else {
-                f[j + k] = (float)(int)v[0][j + k] * (a * s0) + bias;
-            }
-        }
+        f[j] = join<MODE, P, N>(v, j, RowScale{sc.x, sc.y}, s0, s1, bias, o.act);
+        f[j + 1] = join<MODE, P, N>(v, j + 1, RowScale{sc.z, sc.w}, s0, s1, bias, o.act);
     }
     OT* out = static_cast<OT*>(o.out) + t * o.ldo + n;
     if (valid >= N) {
@@ -259,7 +274,7 @@ __device__ __forceinline__ void emit_channel(const ChannelOut& o, const uint32_t
             int32_t* acc = o.acc + m * o.acc_pitch + t * o.rows + n;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                if (j < valid) *acc = (int)v[m][j];
+                if (j < valid) *acc = v[m][j];
                 acc += o.rows;
             }
         }
@@ -450,15 +465,15 @@ __global__ void __launch_bounds__(kTileThreads)
         tc_fence_after_sync();
         const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
         for (int c = 0; c < nv; c += 16) {
-            uint32_t r[kV][16];
+            int r[kV][16];
 #pragma unroll
-            for (int i = 0; i < kV; ++i) tmem_ld16(tl + i * p.nt + c, r[i]);
+            for (int i = 0; i < kV; ++i) tmem_ld16(tl + i * p.nt + c, as_words(r[i]));
             tmem_wait_ld();
             if (split > 1) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
 #pragma unroll
-                    for (int i = 0; i < kV; ++i) part[(i * p.nt + c + j) * 128 + ch] = (int)r[i][j];
+                    for (int i = 0; i < kV; ++i) part[(i * p.nt + c + j) * 128 + ch] = r[i][j];
             } else if (n < p.out_rows) {
                 emit_channel<MODE, P, OT, 16>(co, r, t0 + c, n, nv - c, tok + c, s0, s1, bias);
             }
@@ -472,19 +487,67 @@ __global__ void __launch_bounds__(kTileThreads)
     if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
     if (split > 1) {
         cluster_sync_all();
-        if (warp >= 2 && n < p.out_rows) {
-            // the tokens are dealt to the CTAs in pairs
-            for (int c = 2 * (int)rank; c < nv; c += 2 * (int)split) {
-                uint32_t v[kV][2];
+        // The tokens are dealt to the CTAs, a CTA's to its warps; a lane joins
+        // four channels, every peer's sums of them under way together.
+        const int nq = n0 + 4 * lane;
+        float sq[2][4] = {}, bq[4] = {};
+        if constexpr (MODE != kGrad) {
 #pragma unroll
-                for (int i = 0; i < kV; ++i) v[i][0] = v[i][1] = 0;
-                for (uint32_t q = 0; q < split; ++q)
+            for (int k = 0; k < 4; ++k)
+                if (nq + k < p.out_rows) {
+                    sq[0][k] = __ldg(p.s[0] + nq + k);
+                    if constexpr (MODE == kGated) sq[1][k] = __ldg(p.s[1] + nq + k);
+                    if (MODE == kMatmul && p.bias) bq[k] = __ldg(p.bias + nq + k);
+                }
+        }
+        for (int c = (int)rank + (int)split * warp; c < nv; c += (int)split * (kTileThreads / 32)) {
+            int4 w[8][kV];
 #pragma unroll
-                    for (int i = 0; i < kV; ++i) {
-                        v[i][0] += ld_peer(&part[(i * p.nt + c) * 128 + ch], q);
-                        v[i][1] += ld_peer(&part[(i * p.nt + c + 1) * 128 + ch], q);
+            for (uint32_t q = 0; q < 8; ++q)
+#pragma unroll
+                for (int i = 0; i < kV; ++i)
+                    w[q][i] = q < split ? ld_peer(&part[(i * p.nt + c) * 128 + 4 * lane], q) : make_int4(0, 0, 0, 0);
+            int v[kV][4];
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    v[i][0] += w[q][i].x;
+                    v[i][1] += w[q][i].y;
+                    v[i][2] += w[q][i].z;
+                    v[i][3] += w[q][i].w;
+                }
+            }
+            const RowScale sc = tok[c];
+            const int64_t t = t0 + c;
+            alignas(16) OT o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                o[k] = from_f32<OT>(join<MODE, P>(v, k, sc, sq[0][k], sq[1][k], bq[k], p.act));
+            OT* out = static_cast<OT*>(p.out) + t * p.ldo + nq;
+            if (p.quad && nq + 4 <= p.out_rows) {
+                if constexpr (sizeof(OT) == 4)
+                    *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(o);
+                else
+                    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(o);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (nq + k < p.out_rows) out[k] = o[k];
+            }
+            if (MODE != kGrad && p.acc) {
+#pragma unroll
+                for (int m = 0; m < (MODE == kGated ? 2 : 1); ++m) {
+                    int32_t* acc = p.acc + (m * (int64_t)p.T + t) * p.rows + nq;
+                    if (p.quad && nq + 4 <= p.out_rows) {
+                        *reinterpret_cast<int4*>(acc) = make_int4(v[m][0], v[m][1], v[m][2], v[m][3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (nq + k < p.out_rows) acc[k] = v[m][k];
                     }
-                emit_channel<MODE, P, OT, 2>(co, v, t0 + c, n, nv - c, tok + c, s0, s1, bias);
+                }
             }
         }
         cluster_sync_all();  // the peers have read this CTA's sums
@@ -1125,9 +1188,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             } else {
                 const int nv = (int)min((int64_t)cols, p.T - c0);
                 for (int c = 0; c < nv; c += 16) {
-                    uint32_t v[P][16];
+                    int v[P][16];
 #pragma unroll
-                    for (int i = 0; i < P; ++i) tmem_ld16(tl + i * un.nt + c, v[i]);
+                    for (int i = 0; i < P; ++i) tmem_ld16(tl + i * un.nt + c, as_words(v[i]));
                     tmem_wait_ld();
                     if (r0 < p.out_rows)
                         emit_channel<MODE, P, OT, 16>(co, v, c0 + c, (int)r0, nv - c, ts + c, sa, 0.0f, bias);
@@ -1204,6 +1267,8 @@ static cudaError_t run_tile(const GemmArgs& a, cudaStream_t s) {
     smem += kCtlBytes + 1024;
     if (smem < 456 * p.tmem_cols - 1024) smem = 456 * p.tmem_cols - 1024;
 
+    p.quad = reinterpret_cast<uintptr_t>(a.out) % (4 * sizeof(OT)) == 0 && a.ldo % 4 == 0 &&
+             (!a.acc || (reinterpret_cast<uintptr_t>(a.acc) % 16 == 0 && a.rows % 4 == 0));
     p.direct = 0;
     for (int m = 0; m < a.n_mats; ++m) {
         p.w[m] = a.w[m];
