@@ -11,6 +11,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "moe_dense.cuh"
@@ -1227,8 +1228,91 @@ static cudaError_t allow_smem(K kernel, bool (&done)[64]) {
     return e;
 }
 
+// Clusters of `split` CTAs that run at once, with one or two CTAs on an SM (the
+// GPU's clusters do not cover all of its SMs: of 148, clusters of 8 with a CTA
+// on each SM use 120).
+static int clusters_at_once(bool two, int split) {
+    static int table[64][2][9];
+    static std::once_flag once[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    std::call_once(once[dev], [&] {
+        auto* kernel = k_dense_tile<kMatmul, 1, float>;
+        static bool done[64];
+        const bool ok = allow_smem(kernel, done) == cudaSuccess;
+        for (int t = 0; t < 2; ++t)
+            for (int c = 1; c <= 8; ++c) {
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3(c * 1024);
+                cfg.blockDim = dim3(kTileThreads);
+                cfg.dynamicSmemBytes = (t ? 112 : 200) * 1024;
+                cudaLaunchAttribute at[1];
+                at[0].id = cudaLaunchAttributeClusterDimension;
+                at[0].val.clusterDim.x = c;
+                at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+                cfg.attrs = at;
+                cfg.numAttrs = 1;
+                int n = 0;
+                if (!ok || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
+                    n = (t ? 2 : 1) * (device_info().sm_count * 4 / 5 / c);
+                table[dev][t][c] = n < 1 ? 1 : n;
+            }
+    });
+    return table[dev][two][split];
+}
+
+struct TilePlan {
+    int nt, split, stages, smem;
+    double us;  // estimate
+};
+
+// Tokens of a tile and CTAs of a tile's contraction.  A stage takes about 0.16
+// us (gated 0.3, gradient 0.24) whatever its tokens (it is the latency of what
+// is under way), a tile's end by its columns, the launch and the first loads 5, and with a split the sums' way through shared memory; what
+// does not fit at once runs in rounds.  With 128 tokens, 6144 codes and 2048
+// channels: 64 tokens by 4 CTAs 9.3 us, 128 by 1 17.6 us, 128 by 8 11.4 us, 16
+// by 4 17.1 us.
+template <int MODE, int P>
+static TilePlan plan_tile(int T, int tiles_n, int steps) {
+    constexpr int kA = MODE == kGated ? 2 : 1, kV = MODE == kGated ? 2 : P;
+    const int sms = device_info().sm_count;
+    TilePlan best{};
+    double least = 1e30;
+    for (int nt = 16; nt <= (P == 3 ? 64 : 128); nt *= 2) {
+        const int64_t tiles = (int64_t)tiles_n * ((T + nt - 1) / nt);
+        const int cols = kV * nt, stage = kA * kTileRows * kStageK + P * nt * kStageK;
+        const int tmem = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+        for (int split : {1, 2, 3, 4, 6, 8}) {
+            if (split > steps) break;
+            const int per_cta = (steps + split - 1) / split;
+            int stages = 108 * 1024 / stage;
+            stages = stages > kMaxStages ? kMaxStages : stages;
+            stages = stages > per_cta ? per_cta : stages;
+            // Shared memory in proportion to the TMEM columns, so that the CTAs
+            // that fit an SM together also find their columns there.
+            int smem = stages * stage;
+            if (split > 1 && smem < cols * 512) smem = cols * 512;
+            smem += kCtlBytes + 1024;
+            if (smem < 456 * tmem - 1024) smem = 456 * tmem - 1024;
+            const int at_once = clusters_at_once(smem <= 112 * 1024, split);
+            const int64_t rounds = (tiles + at_once - 1) / at_once;
+            const double ctas = (double)(tiles < at_once ? tiles : at_once) * split;
+            const double share = ctas > sms ? ctas / sms : 1.0;  // CTAs that share an SM
+            const double k = kV == 1 ? 1.0 : kV == 2 ? 1.7 : 2.4;
+            const double end = split == 1 ? 1.5 + 0.023 * nt * k : 0.3 + (0.016 + 0.045 / split) * nt * k;
+            const double stage_us = MODE == kGated ? 0.3 : MODE == kGrad ? 0.24 : 0.16;
+            const double us = 5.0 + rounds * share * (per_cta * stage_us + end);
+            if (us < least) {
+                least = us;
+                best = TilePlan{nt, split, stages, smem, us};
+            }
+        }
+    }
+    return best;
+}
+
 template <int MODE, int P, typename OT>
-static cudaError_t run_tile(const GemmArgs& a, cudaStream_t s) {
+static cudaError_t run_tile(const GemmArgs& a, const TilePlan& plan, cudaStream_t s) {
     static bool attr_done[64];
     cudaError_t e = allow_smem(k_dense_tile<MODE, P, OT>, attr_done);
     if (e != cudaSuccess) return e;
@@ -1240,33 +1324,15 @@ static cudaError_t run_tile(const GemmArgs& a, cudaStream_t s) {
     p.out_rows = MODE == kGrad ? a.cols : a.rows;
     p.k_steps = ((MODE == kGrad ? a.rows : a.cols) + kStageK - 1) / kStageK;
     p.steps = p.k_steps * (MODE == kGrad ? a.n_mats : 1);
-    const int nt_max = P == 3 ? 64 : 128;
-    p.nt = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : nt_max;
+    p.tiles_n = (p.out_rows + kTileRows - 1) / kTileRows;
+    const int split = plan.split, smem = plan.smem;
+    p.nt = plan.nt;
+    p.stages = plan.stages;
     const int cols = (MODE == kGated ? 2 : P) * p.nt;
     p.tmem_cols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
-    p.tiles_n = (p.out_rows + kTileRows - 1) / kTileRows;
-    const int64_t tiles = (int64_t)p.tiles_n * ((a.T + p.nt - 1) / p.nt);
-    const int sms = device_info().sm_count;
-    int split = 1;
-    if (tiles < sms) {
-        split = (int)(sms / tiles);
-        split = split > 8 ? 8 : split;
-        split = split > p.steps ? p.steps : split;
-    }
-    if (tiles * split > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.stage_bytes = kA * kTileRows * kStageK + P * p.nt * kStageK;
-    const int per_cta = (p.steps + split - 1) / split;
-    const int budget = (tiles * split <= sms ? 200 : 108) * 1024;
-    p.stages = budget / p.stage_bytes;
-    p.stages = p.stages > kMaxStages ? kMaxStages : p.stages;
-    p.stages = p.stages > per_cta ? per_cta : p.stages;
-    // Shared memory in proportion to the TMEM columns, so that the CTAs that
-    // fit an SM together also find their columns there.
-    int smem = p.stages * p.stage_bytes;
-    if (split > 1 && smem < cols * 512) smem = cols * 512;
-    smem += kCtlBytes + 1024;
-    if (smem < 456 * p.tmem_cols - 1024) smem = 456 * p.tmem_cols - 1024;
-
+    const int64_t tiles = (int64_t)p.tiles_n * ((a.T + p.nt - 1) / p.nt);
+    if (tiles * split > 0x7FFFFFFF) return cudaErrorInvalidValue;
     p.quad = reinterpret_cast<uintptr_t>(a.out) % (4 * sizeof(OT)) == 0 && a.ldo % 4 == 0 &&
              (!a.acc || (reinterpret_cast<uintptr_t>(a.acc) % 16 == 0 && a.rows % 4 == 0));
     p.direct = 0;
@@ -1317,8 +1383,44 @@ static cudaError_t run_tile(const GemmArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k_dense_tile<MODE, P, OT>, wm[0], wm[1], xm, p);
 }
 
+// Columns of a pair's tile (channels of the gated block, tokens elsewhere).
+template <int MODE, int P>
+constexpr int pair_columns = MODE == kGated ? 128 : MODE == kMatmul ? 256 : P == 2 ? 128 : 64;
+
+struct PairPlan {
+    int tiles_r, parts;
+    int64_t whole, units;
+    double us;  // estimate
+};
+
+// The tiles after the last full round of the pairs are cut into column parts
+// where that ends sooner: a stage takes 0.27 us of a whole tile, 0.24 of a half
+// and 0.235 of a quarter (by then it is latency), the last epilogue 4, 1.5 and 1.
+template <int MODE, int P>
+static PairPlan plan_pair(int T, int out_rows, int steps) {
+    constexpr int nt = pair_columns<MODE, P>;
+    const int64_t pairs = device_info().sm_count / 2;
+    PairPlan p;
+    p.tiles_r = ((MODE == kGated ? T : out_rows) + kPairRows - 1) / kPairRows;
+    const int64_t tiles = (int64_t)p.tiles_r * (((MODE == kGated ? out_rows : T) + nt - 1) / nt);
+    p.whole = tiles / pairs * pairs;
+    const int64_t rest = tiles - p.whole;
+    p.parts = 1;
+    double end = rest ? 0.27 * steps + 4.0 : 4.0;
+    for (int q = 2; rest && q <= (P == 3 ? 2 : 4); q *= 2) {
+        const double cost = (double)((rest * q + pairs - 1) / pairs) * steps * (q == 2 ? 0.24 : 0.235) + (q == 2 ? 1.5 : 1.0);
+        if (cost < end) {
+            end = cost;
+            p.parts = q;
+        }
+    }
+    p.units = p.whole + rest * p.parts;
+    p.us = 4.0 + (double)(p.whole / pairs) * steps * 0.27 + end;
+    return p;
+}
+
 template <int MODE, int P, typename OT>
-static cudaError_t run_pair(const GemmArgs& a, cudaStream_t s) {
+static cudaError_t run_pair(const GemmArgs& a, const PairPlan& plan, cudaStream_t s) {
     static bool attr_done[64];
     cudaError_t e = allow_smem(k_dense_pair<MODE, P, OT>, attr_done);
     if (e != cudaSuccess) return e;
@@ -1342,25 +1444,11 @@ static cudaError_t run_pair(const GemmArgs& a, cudaStream_t s) {
     const int esz = a.dtype == MOE_F32 ? 4 : 2;
     p.vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ldo * esz % 16 == 0 && a.rows * esz % 16 == 0 &&
             (!a.acc || (reinterpret_cast<uintptr_t>(a.acc) % 16 == 0 && a.rows % 4 == 0));
-    p.nt = MODE == kGated ? 128 : MODE == kMatmul ? 256 : P == 2 ? 128 : 64;
-    p.tiles_r = ((MODE == kGated ? a.T : p.out_rows) + kPairRows - 1) / kPairRows;
-    const int64_t tiles = (int64_t)p.tiles_r * (((MODE == kGated ? a.rows : a.T) + p.nt - 1) / p.nt);
-    // The tiles after the last full round of the pairs are cut into column
-    // parts where that ends sooner: a half costs 0.55 and a quarter 0.35 of a
-    // tile (the 256-row operand is loaded and read again for each part).
-    const int64_t pairs = device_info().sm_count / 2;
-    p.whole = tiles / pairs * pairs;
-    const int64_t rest = tiles - p.whole;
-    p.parts = 1;
-    double best = rest ? 1.0 : 0.0;
-    for (int q = 2; q <= (P == 3 ? 2 : 4); q *= 2) {
-        const double cost = (double)((rest * q + pairs - 1) / pairs) * (q == 2 ? 0.55 : 0.35);
-        if (cost < best) {
-            best = cost;
-            p.parts = q;
-        }
-    }
-    p.units = p.whole + rest * p.parts;
+    p.nt = pair_columns<MODE, P>;
+    p.tiles_r = plan.tiles_r;
+    p.whole = plan.whole;
+    p.parts = plan.parts;
+    p.units = plan.units;
     // boxes: the MMA's rows are 128 a CTA, its columns half of the pair's
     PairMaps maps;
     auto map_w = [&](CUtensorMap* m, int i, int box) {
@@ -1390,6 +1478,7 @@ static cudaError_t run_pair(const GemmArgs& a, cudaStream_t s) {
         for (int m = 0; m < 2; ++m) maps.small[m] = maps.b[m];
     else if (MODE != kGated)
         maps.small[1] = maps.small[0];
+    const int64_t pairs = device_info().sm_count / 2;
     const unsigned grid = 2 * (unsigned)(p.units < pairs ? p.units : pairs);
     k_dense_pair<MODE, P, OT><<<grid, kPairThreads, kPairSmem<MODE>, s>>>(maps, p);
     return cudaGetLastError();
@@ -1472,12 +1561,19 @@ static cudaError_t run_few(const GemmArgs& a, const void* x, int x_type, bool de
     return by_size(__half());
 }
 
-// Pairs from this many tokens on.
-constexpr int kPairTokens = 256;
 
+// Single CTAs or pairs, by their estimates (within 15 % of the better one over 17
+// to 4096 tokens of five layer shapes; below 64 tokens a pair's rows stay empty).
 template <int MODE, int P, typename OT>
 static cudaError_t run_product(const GemmArgs& a, cudaStream_t s) {
-    return a.T >= kPairTokens && tma_operands(a) ? run_pair<MODE, P, OT>(a, s) : run_tile<MODE, P, OT>(a, s);
+    const int out_rows = MODE == kGrad ? a.cols : a.rows;
+    const int steps = ((MODE == kGrad ? a.rows : a.cols) + kStageK - 1) / kStageK * (MODE == kGrad ? a.n_mats : 1);
+    const TilePlan tile = plan_tile<MODE, P>(a.T, (out_rows + kTileRows - 1) / kTileRows, steps);
+    if (a.T >= 64 && tma_operands(a)) {
+        const PairPlan pair = plan_pair<MODE, P>(a.T, out_rows, steps);
+        if (pair.us < tile.us) return run_pair<MODE, P, OT>(a, pair, s);
+    }
+    return run_tile<MODE, P, OT>(a, tile, s);
 }
 
 template <int MODE>

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 DT = dh.DTYPES
 # tokens, cols, rows: one of everything, sizes around the tiles (16, 32, 64, 128 tokens, 128 rows, 128 codes),
 # odd ones whose rows are no multiple of 16, 8 or 4 bytes, long rows
-SIZES = [(1, 1, 1), (1, 16, 1), (1, 6144, 300), (2, 127, 5), (3, 129, 130), (4, 512, 128), (5, 2048, 257),
+SIZES = [(24, 1040, 300), (32, 272, 65), (20, 999, 77), (1, 1, 1), (1, 16, 1), (1, 6144, 300), (2, 127, 5), (3, 129, 130), (4, 512, 128), (5, 2048, 257),
          (16, 1000, 77), (17, 128, 384), (33, 100, 64), (64, 1040, 129), (65, 36, 127), (128, 256, 128),
          (129, 260, 131), (300, 1000, 500), (257, 1536, 640)]
 LARGE = [(700, 2048, 1504), (1030, 1024, 528), (513, 272, 1032), (256, 16, 16), (2500, 128, 4000), (4000, 1040, 3120), (40, 64, 6200), (30, 48, 7001), (21, 32, 16500), (600, 64, 8192)]
@@ -123,10 +123,10 @@ def ffn_inputs(T, H, I, dtype):
     return x, ws, ss
 
 
-# (300, ..) and up run the tiled kernels, 5 to 16 the weight stream with tokens quantised inside, and
+# (300, ..) and up run the tiled kernels, up to 32 the weight stream with tokens quantised inside, and
 # 1000 x 500 and 36 x 20 rows off the 16-byte grid
 FFN = [(1, 256, 128), (1, 6144, 2048), (3, 512, 96), (4, 6144, 2048), (5, 1000, 500), (8, 1024, 304), (9, 1024, 304),
-       (16, 2048, 640), (17, 512, 256), (2, 36, 20), (300, 1024, 512), (130, 264, 72)]
+       (16, 2048, 640), (17, 512, 256), (25, 1024, 208), (32, 512, 272), (2, 36, 20), (300, 1024, 512), (130, 264, 72)]
 
 
 @pytest.mark.parametrize("T,H,I", FFN)
