@@ -206,6 +206,31 @@ struct RowScale {
 };
 
 // ---------------------------------------------------------------------------
+// Launches.  Every dense kernel may start while the kernel before it on the
+// stream ends (programmatic dependent launch): it waits (pdl_wait) before it
+// touches memory that others write, and lets its own successor start once it
+// runs, so that launches and prologues of a chain overlap.
+// ---------------------------------------------------------------------------
+template <typename... P, typename... A>
+cudaError_t launch_dense(void (*kernel)(P...), unsigned grid, int threads, size_t smem, int cluster, cudaStream_t s,
+                         A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// ---------------------------------------------------------------------------
 // The tiled product kernel (moe_dense_gemm.cu)
 // ---------------------------------------------------------------------------
 enum GemmMode { kMatmul = 0, kGated = 1, kGrad = 2 };
@@ -238,7 +263,8 @@ cudaError_t launch_matmul(const GemmArgs& a, cudaStream_t s);
 cudaError_t launch_gated(const GemmArgs& a, cudaStream_t s);
 // The products of up to a few float tokens (rows of x with stride a.ldx, type
 // x_type), quantised inside the kernel; for operands that few_quantised_fits.
-// dependent: the kernel may start while the one before it on the stream ends.
+// dependent: the kernel before it on the stream is a dense product that does not
+// write the weights, so that they may be read before it ends.
 bool few_quantised_fits(const GemmArgs& a, const void* x, int x_type);
 cudaError_t launch_matmul_quantised(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s);
 cudaError_t launch_gated_quantised(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s);
@@ -265,10 +291,14 @@ struct GradRowsArgs {
     int64_t pitch;
     RowScale* scale;   // [T]
     float* partials;   // [grid][2][N] column sums
-    float* colsum[2];  // gated: ds_gate, ds_up; matmul: ds, dbias (each may be null)
 };
 int grad_rows_grid(int T);
-cudaError_t launch_grad_rows(const GradRowsArgs& a, cudaStream_t s);
+// n_part: how many partial sums of each column there are.
+cudaError_t launch_grad_rows(const GradRowsArgs& a, int* n_part, cudaStream_t s);
+// The column sums (gated: ds_gate, ds_up; matmul: ds, dbias; each may be null)
+// from the partials.  Follows the gradient's product on the stream and runs
+// beside it: the partials were complete before that product began.
+cudaError_t launch_col_sums(const float* partials, int n_part, int N, float* out0, float* out1, cudaStream_t s);
 
 }  // namespace dense
 }  // namespace moe

@@ -90,15 +90,14 @@ static int backward(int n_mats, const void* dy, int dtype, int64_t lddy, const i
     r.pitch = L.pitch;
     r.scale = reinterpret_cast<RowScale*>(ws + L.scale);
     r.partials = reinterpret_cast<float*>(ws + L.partials);
-    r.colsum[0] = sum0;
-    r.colsum[1] = sum1;
     GemmArgs g{};
     for (int m = 0; m < n_mats; ++m) {
         r.s[m] = sc[m];
         g.w[m] = w[m];
         g.ldw[m] = ldw[m];
     }
-    int st = status_of(launch_grad_rows(r, s));
+    int n_part = 0;
+    int st = status_of(launch_grad_rows(r, &n_part, s));
     if (st) return st;
     g.n_mats = n_mats;
     g.rows = rows;
@@ -112,7 +111,9 @@ static int backward(int n_mats, const void* dy, int dtype, int64_t lddy, const i
     g.out = dx;
     g.ldo = lddx;
     g.dtype = dtype;
-    return status_of(launch_grad_matmul(g, s));
+    st = status_of(launch_grad_matmul(g, s));
+    if (!st && (sum0 || sum1)) st = status_of(launch_col_sums(r.partials, n_part, rows, sum0, sum1, s));
+    return st;
 }
 
 struct FfnLayout {

@@ -325,6 +325,8 @@ __global__ void __launch_bounds__(kTileThreads)
         tmem_alloc(tmem_slot, p.tmem_cols);
         tmem_relinquish();
     }
+    pdl_wait();
+    pdl_launch_dependents();
     for (int i = threadIdx.x; i < p.nt; i += kTileThreads)
         tok[i] = i >= nv ? RowScale{0.0f, 0.0f} : MODE == kGrad ? p.gscale[t0 + i] : RowScale{p.xd[t0 + i], 1.0f};
     tc_fence_before_sync();
@@ -589,7 +591,7 @@ struct FewParams {
     int pitch;   // QUANT: bytes of a token's codes in shared memory
     int act, dtype;
     int w_unit[kMaxMats], x_unit;
-    bool dependent;  // launched early: wait for the kernel before it
+    bool dependent;  // the kernel before this one does not write the weights
 };
 
 __device__ __forceinline__ void mma_16832(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -634,11 +636,13 @@ __global__ void __launch_bounds__(32 * WARPS) k_dense_few(const FewParams p) {
                                              : load16(wr[m][h], c, p.cols, p.w_unit[m]);
         }
     };
+    if (!p.dependent) pdl_wait();
     load_w(warp);
+    if (p.dependent) pdl_wait();
+    pdl_launch_dependents();
     if constexpr (QUANT) {
         if (threadIdx.x < 8 * NB) peak[threadIdx.x] = 0;
         __syncthreads();
-        if (p.dependent) pdl_wait();
         // `per` warps a token (one warp takes every WARPS-th token where there are
         // more): its vectors loaded together and kept for the second pass
         constexpr int V = 16 / (int)sizeof(XT), kKeep = 8;
@@ -735,7 +739,6 @@ __global__ void __launch_bounds__(32 * WARPS) k_dense_few(const FewParams p) {
             }
         }
     }
-    pdl_launch_dependents();
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -996,6 +999,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     cluster_sync_all();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -1369,18 +1374,7 @@ static cudaError_t run_tile(const GemmArgs& a, const TilePlan& plan, cudaStream_
                       (uint64_t)a.planes * a.T, a.ldx, kStageK, p.nt, CU_TENSOR_MAP_SWIZZLE_128B);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * split));
-    cfg.blockDim = dim3(kTileThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_dense_tile<MODE, P, OT>, wm[0], wm[1], xm, p);
+    return launch_dense(k_dense_tile<MODE, P, OT>, (unsigned)(tiles * split), kTileThreads, smem, split, s, wm[0], wm[1], xm, p);
 }
 
 // Columns of a pair's tile (channels of the gated block, tokens elsewhere).
@@ -1480,8 +1474,7 @@ static cudaError_t run_pair(const GemmArgs& a, const PairPlan& plan, cudaStream_
         maps.small[1] = maps.small[0];
     const int64_t pairs = device_info().sm_count / 2;
     const unsigned grid = 2 * (unsigned)(p.units < pairs ? p.units : pairs);
-    k_dense_pair<MODE, P, OT><<<grid, kPairThreads, kPairSmem<MODE>, s>>>(maps, p);
-    return cudaGetLastError();
+    return launch_dense(k_dense_pair<MODE, P, OT>, grid, kPairThreads, kPairSmem<MODE>, 1, s, maps, p);
 }
 
 // Whether TMA can take every operand: addresses and row strides on 16 bytes.
@@ -1527,17 +1520,8 @@ static cudaError_t run_few(const GemmArgs& a, const void* x, int x_type, bool de
         static bool attr_done[64];
         cudaError_t e = allow_smem(kernel, attr_done);
         if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(grid);
-        cfg.blockDim = dim3(32 * WARPS);
-        cfg.dynamicSmemBytes = WARPS * (MODE == kGated ? 2 : 1) * NB * 512 + (x_type < 0 ? 0 : 32 * NB + (size_t)a.T * p.pitch);
-        cfg.stream = s;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = dependent ? 1 : 0;
-        return cudaLaunchKernelEx(&cfg, kernel, p);
+        const size_t smem = WARPS * (MODE == kGated ? 2 : 1) * NB * 512 + (x_type < 0 ? 0 : 32 * NB + (size_t)a.T * p.pitch);
+        return launch_dense(kernel, grid, 32 * WARPS, smem, 1, s, p);
     };
     using std::integral_constant;
     // 16 warps a CTA where the rows give the SMs less than two CTAs each
@@ -1562,7 +1546,7 @@ static cudaError_t run_few(const GemmArgs& a, const void* x, int x_type, bool de
 }
 
 
-// Single CTAs or pairs, by their estimates (within 15 % of the better one over 17
+// Single CTAs or pairs, by their estimates (within 20 % of the better one over 17
 // to 4096 tokens of five layer shapes; below 64 tokens a pair's rows stay empty).
 template <int MODE, int P, typename OT>
 static cudaError_t run_product(const GemmArgs& a, cudaStream_t s) {

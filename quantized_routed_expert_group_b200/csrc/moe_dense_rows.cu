@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(512)
                      int64_t ldq, float* __restrict__ d) {
     using T = typename Elem<DT>::T;
     __shared__ uint32_t sh[64];
+    pdl_wait();
+    pdl_launch_dependents();
     const int64_t row = blockIdx.x;
     const T* xr = x + row * ldx;
     int8_t* qr = q + row * ldq;
@@ -97,11 +99,11 @@ static cudaError_t quantize_token(const void* x, int64_t rows, int cols, int64_t
     for (int64_t r = 0; r < rows; r += 1 << 30) {  // the grid's limit
         const unsigned grid = (unsigned)(rows - r < (1 << 30) ? rows - r : (1 << 30));
         const T* xr = static_cast<const T*>(x) + r * ldx;
+        cudaError_t e;
         if (vec)
-            k_quantize_token<DT, kVec><<<grid, threads, 0, s>>>(xr, ldx, cols, q + r * ldq, ldq, d + r);
+            e = launch_dense(k_quantize_token<DT, kVec>, grid, threads, 0, 1, s, xr, ldx, cols, q + r * ldq, ldq, d + r);
         else
-            k_quantize_token<DT, 1><<<grid, threads, 0, s>>>(xr, ldx, cols, q + r * ldq, ldq, d + r);
-        const cudaError_t e = cudaGetLastError();
+            e = launch_dense(k_quantize_token<DT, 1>, grid, threads, 0, 1, s, xr, ldx, cols, q + r * ldq, ldq, d + r);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -226,6 +228,8 @@ template <int MATS, int DT, int VEC, int NJ>
 __global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_grad_rows(const GradRowsParams p) {
     constexpr int P = planes_of(DT);
     __shared__ uint32_t sh[64];
+    pdl_wait();
+    pdl_launch_dependents();
     GradIn<MATS, DT, VEC> in[NJ];
     Raw<float, VEC> sc[NJ][MATS];
     float sum[NJ][2][VEC], xd_next = 0.0f;
@@ -301,6 +305,8 @@ template <int MATS, int DT>
 __global__ void __launch_bounds__(1024) k_grad_rows_long(const GradRowsParams p) {
     constexpr int P = planes_of(DT);
     __shared__ uint32_t sh[64];
+    pdl_wait();
+    pdl_launch_dependents();
     float* part = p.partials + (int64_t)blockIdx.x * 2 * p.N;
     int buf = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
@@ -337,24 +343,43 @@ __global__ void __launch_bounds__(1024) k_grad_rows_long(const GradRowsParams p)
     }
 }
 
-// out[c] = sum over the CTAs' partial sums, 32 columns a CTA: each of its 32
-// warps adds every 32nd partial in fp64, then the warps' sums are added in order.
-__global__ void __launch_bounds__(1024) k_col_sums(const float* __restrict__ partials, int n_part, int N,
-                                                   float* __restrict__ out0, float* __restrict__ out1) {
-    __shared__ double sh[32][33];
+// out[c] = sum over the CTAs' partial sums, 32 columns a CTA: each of its 8
+// warps adds every 8th partial in fp64, then the warps' sums are added in order.
+// It runs under the gradient's product (small CTAs, no shared memory to speak
+// of), whose end it waits for last, so that whatever follows finds both done.
+__global__ void __launch_bounds__(256) k_col_sums(const float* __restrict__ partials, int n_part, int N,
+                                                  float* __restrict__ out0, float* __restrict__ out1) {
+    __shared__ double sh[8][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, k = blockIdx.y;
     float* out = k ? out1 : out0;
-    if (!out) return;
-    double a = 0.0;
-    if (c < N)
-        for (int i = warp; i < n_part; i += 32) a += (double)partials[((int64_t)i * 2 + k) * N + c];
-    sh[warp][lane] = a;
-    __syncthreads();
-    if (warp == 0 && c < N) {
-        for (int i = 1; i < 32; ++i) a += sh[i][lane];
-        out[c] = (float)a;
+    if (out) {
+        double a = 0.0;
+        if (c < N) {
+#pragma unroll 8
+            for (int i = warp; i < n_part; i += 8) a += (double)partials[((int64_t)i * 2 + k) * N + c];
+        }
+        sh[warp][lane] = a;
+        __syncthreads();
+        if (warp == 0 && c < N) {
+            for (int i = 1; i < 8; ++i) a += sh[i][lane];
+            out[c] = (float)a;
+        }
     }
+    pdl_wait();
+}
+
+cudaError_t launch_col_sums(const float* partials, int n_part, int N, float* out0, float* out1, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((N + 31) / 32), 2);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_col_sums, partials, n_part, N, out0, out1);
 }
 
 // CTAs of the gradient row kernel: a fixed grid (the column sums' order is the
@@ -378,21 +403,18 @@ static cudaError_t grad_rows(const GradRowsArgs& a, GradRowsParams p, int& grid,
     const int per = vec ? (groups <= 2 * 768 ? 2 : 4) : (groups <= 512 ? 1 : 4);
     const int threads = (groups + 32 * per - 1) / (32 * per) * 32;
     if (threads > (vec ? (per == 2 ? 768 : 512) : 1024)) {
-        k_grad_rows_long<MATS, DT><<<grid, 1024, 0, s>>>(p);
-        return cudaGetLastError();
+        return launch_dense(k_grad_rows_long<MATS, DT>, grid, 1024, 0, 1, s, p);
     }
     const int per_sm = threads > 384 ? 1 : threads > 256 ? 2 : threads > 192 ? 3 : 4;
     if (grid > per_sm * device_info().sm_count) grid = per_sm * device_info().sm_count;
     if (vec)
-        per == 2 ? k_grad_rows<MATS, DT, 4, 2><<<grid, threads, 0, s>>>(p)
-                 : k_grad_rows<MATS, DT, 4, 4><<<grid, threads, 0, s>>>(p);
-    else
-        per == 1 ? k_grad_rows<MATS, DT, 1, 1><<<grid, threads, 0, s>>>(p)
-                 : k_grad_rows<MATS, DT, 1, 4><<<grid, threads, 0, s>>>(p);
-    return cudaGetLastError();
+        return per == 2 ? launch_dense(k_grad_rows<MATS, DT, 4, 2>, grid, threads, 0, 1, s, p)
+                        : launch_dense(k_grad_rows<MATS, DT, 4, 4>, grid, threads, 0, 1, s, p);
+    return per == 1 ? launch_dense(k_grad_rows<MATS, DT, 1, 1>, grid, threads, 0, 1, s, p)
+                    : launch_dense(k_grad_rows<MATS, DT, 1, 4>, grid, threads, 0, 1, s, p);
 }
 
-cudaError_t launch_grad_rows(const GradRowsArgs& a, cudaStream_t s) {
+cudaError_t launch_grad_rows(const GradRowsArgs& a, int* n_part, cudaStream_t s) {
     GradRowsParams p{};
     p.dy = a.dy;
     p.lddy = a.lddy;
@@ -417,9 +439,8 @@ cudaError_t launch_grad_rows(const GradRowsArgs& a, cudaStream_t s) {
         e = a.dtype == MOE_F32    ? grad_rows<1, MOE_F32>(a, p, grid, s)
             : a.dtype == MOE_BF16 ? grad_rows<1, MOE_BF16>(a, p, grid, s)
                                   : grad_rows<1, MOE_F16>(a, p, grid, s);
-    if (e != cudaSuccess || (!a.colsum[0] && !a.colsum[1])) return e;
-    k_col_sums<<<dim3((unsigned)((a.N + 31) / 32), 2), 1024, 0, s>>>(p.partials, grid, a.N, a.colsum[0], a.colsum[1]);
-    return cudaGetLastError();
+    *n_part = grid;
+    return e;
 }
 
 }  // namespace dense
