@@ -79,23 +79,35 @@ __device__ __forceinline__ void store_elem(void* out, int64_t i, int dtype, floa
 constexpr float kGelu0 = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGelu1 = 0.044715f;
 
-__device__ __forceinline__ float act_value(int act, float g) {
-    const float z = act == MOE_ACT_SILU ? g : kGelu0 * (g + kGelu1 * g * g * g);
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
+    const float z = ACT == MOE_ACT_SILU ? g : kGelu0 * (g + kGelu1 * g * g * g);
     const float e = expf(-fabsf(z));
     const float r = __fdividef(1.0f, 1.0f + e);
     return g * (z >= 0.0f ? r : e * r);
 }
 
-__device__ __forceinline__ void act_value_grad(int act, float g, float& a, float& da) {
-    const float z = act == MOE_ACT_SILU ? g : kGelu0 * (g + kGelu1 * g * g * g);
-    const float dz = act == MOE_ACT_SILU ? 1.0f : kGelu0 * (1.0f + 3.0f * kGelu1 * g * g);
+template <int ACT>
+__device__ __forceinline__ void act_value_grad(float g, float& a, float& da) {
+    const float z = ACT == MOE_ACT_SILU ? g : kGelu0 * (g + kGelu1 * g * g * g);
     const float e = expf(-fabsf(z));
     const float r = __fdividef(1.0f, 1.0f + e);
     const float sig = z >= 0.0f ? r : e * r;
     const float dsig = e * r * r;
     a = g * sig;
-    // far out the derivative of the sigmoid is zero while dz may be infinite
-    da = sig + (dsig == 0.0f ? 0.0f : g * dsig * dz);
+    // far out the derivative of the sigmoid is zero while g or dz may be infinite
+    const float gd = ACT == MOE_ACT_SILU ? g : g * (kGelu0 * (1.0f + 3.0f * kGelu1 * g * g));
+    da = sig + (dsig == 0.0f ? 0.0f : gd * dsig);
+}
+
+// f(integral constant ACT) with the activation as a compile-time value, so that
+// a kernel pays for the one it runs.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+    if (act == MOE_ACT_SILU)
+        f(std::integral_constant<int, MOE_ACT_SILU>());
+    else
+        f(std::integral_constant<int, MOE_ACT_GELU>());
 }
 
 // ---------------------------------------------------------------------------

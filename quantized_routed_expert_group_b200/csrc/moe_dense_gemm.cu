@@ -225,9 +225,9 @@ struct ChannelOut {
 
 // A result from its integer sums v[.][j] (gated: gate and up; gradient: the
 // planes) and scales: the token's, the channel's, the bias.
-template <int MODE, int P, int N>
+template <int MODE, int P, int ACT, int N>
 __device__ __forceinline__ float join(const int (&v)[MODE == kGated ? 2 : P][N], int j, const RowScale tok, float s0,
-                                      float s1, float bias, int act) {
+                                      float s1, float bias) {
     if constexpr (MODE == kGrad) {
         // digits joined in fp32: each plane's sum rounds by 2^-24 of itself
         float d = (float)v[P - 1][j];
@@ -235,7 +235,7 @@ __device__ __forceinline__ float join(const int (&v)[MODE == kGated ? 2 : P][N],
         for (int i = P - 2; i >= 0; --i) d = fmaf(d, 256.0f, (float)v[i][j]);
         return d * tok.a * tok.b;
     } else if constexpr (MODE == kGated) {
-        return act_value(act, (float)v[0][j] * (tok.a * s0)) * ((float)v[1][j] * (tok.a * s1));
+        return act_value<ACT>((float)v[0][j] * (tok.a * s0)) * ((float)v[1][j] * (tok.a * s1));
     } else {
         return (float)v[0][j] * (tok.a * s0) + bias;
     }
@@ -249,12 +249,15 @@ template <int MODE, int P, typename OT, int N>
 __device__ __forceinline__ void emit_channel(const ChannelOut& o, const int (&v)[MODE == kGated ? 2 : P][N], int64_t t,
                                              int n, int valid, const RowScale* ts, float s0, float s1, float bias) {
     float f[N];
+    with_act(MODE == kGated ? o.act : MOE_ACT_SILU, [&](auto act) {
+        constexpr int A = decltype(act)::value;
 #pragma unroll
-    for (int j = 0; j < N; j += 2) {
-        const float4 sc = *reinterpret_cast<const float4*>(ts + j);
-        f[j] = join<MODE, P, N>(v, j, RowScale{sc.x, sc.y}, s0, s1, bias, o.act);
-        f[j + 1] = join<MODE, P, N>(v, j + 1, RowScale{sc.z, sc.w}, s0, s1, bias, o.act);
-    }
+        for (int j = 0; j < N; j += 2) {
+            const float4 sc = *reinterpret_cast<const float4*>(ts + j);
+            f[j] = join<MODE, P, A, N>(v, j, RowScale{sc.x, sc.y}, s0, s1, bias);
+            f[j + 1] = join<MODE, P, A, N>(v, j + 1, RowScale{sc.z, sc.w}, s0, s1, bias);
+        }
+    });
     OT* out = static_cast<OT*>(o.out) + t * o.ldo + n;
     if (valid >= N) {
 #pragma unroll
@@ -525,9 +528,11 @@ __global__ void __launch_bounds__(kTileThreads)
             const RowScale sc = tok[c];
             const int64_t t = t0 + c;
             alignas(16) OT o[4];
+            with_act(MODE == kGated ? p.act : MOE_ACT_SILU, [&](auto act) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                o[k] = from_f32<OT>(join<MODE, P>(v, k, sc, sq[0][k], sq[1][k], bq[k], p.act));
+                for (int k = 0; k < 4; ++k)
+                    o[k] = from_f32<OT>(join<MODE, P, decltype(act)::value>(v, k, sc, sq[0][k], sq[1][k], bq[k]));
+            });
             OT* out = static_cast<OT*>(p.out) + t * p.ldo + nq;
             if (p.quad && nq + 4 <= p.out_rows) {
                 if constexpr (sizeof(OT) == 4)
@@ -761,7 +766,9 @@ __global__ void __launch_bounds__(32 * WARPS) k_dense_few(const FewParams p) {
         const float xd = QUANT ? quant_scale(peak[t]).scale : p.xd[t];
         float y = (float)v[0] * (xd * p.s[0][row]);
         if constexpr (MODE == kGated)
-            y = act_value(p.act, y) * ((float)v[M - 1] * (xd * p.s[M - 1][row]));
+            with_act(p.act, [&](auto act) {
+                y = act_value<decltype(act)::value>(y) * ((float)v[M - 1] * (xd * p.s[M - 1][row]));
+            });
         else if (p.bias)
             y += p.bias[row];
         store_elem(p.out, t * p.ldo + row, p.dtype, y);
@@ -1163,12 +1170,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                          stage, lane);
                         }
                         alignas(16) OT h[32];
+                        with_act(p.act, [&](auto act) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const RowScale sc = ts[c + j];
-                            h[j] = from_f32<OT>(act_value(p.act, (float)(int)g[j] * (sa * sc.a)) *
-                                                ((float)(int)u[j] * (sa * sc.b)));
-                        }
+                            for (int j = 0; j < 32; ++j) {
+                                const RowScale sc = ts[c + j];
+                                h[j] = from_f32<OT>(
+                                    act_value<decltype(act)::value>((float)(int)g[j] * (sa * sc.a)) *
+                                    ((float)(int)u[j] * (sa * sc.b)));
+                            }
+                        });
                         store_rows32(static_cast<OT*>(p.out), p.ldo, p.T, p.rows, t0, (int)c0 + c, h, stage, lane);
                     }
                 }
@@ -1179,11 +1189,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     tmem_wait_ld();
                     if (r0 < p.T) {
                         float h[16];
+                        with_act(p.act, [&](auto act) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const RowScale sc = ts[c + j];
-                            h[j] = act_value(p.act, (float)(int)g[j] * (sa * sc.a)) * ((float)(int)u[j] * (sa * sc.b));
-                        }
+                            for (int j = 0; j < 16; ++j) {
+                                const RowScale sc = ts[c + j];
+                                h[j] = act_value<decltype(act)::value>((float)(int)g[j] * (sa * sc.a)) *
+                                       ((float)(int)u[j] * (sa * sc.b));
+                            }
+                        });
                         store16<OT>(p, r0, (int)c0 + c, h);
                         if (p.acc) {
                             store_acc16(p, p.acc + r0 * p.rows, (int)c0 + c, g);

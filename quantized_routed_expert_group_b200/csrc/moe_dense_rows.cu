@@ -157,7 +157,7 @@ struct GradIn {
 };
 
 // Their values and column contributions.
-template <int MATS, int DT, int VEC>
+template <int ACT, int MATS, int DT, int VEC>
 __device__ __forceinline__ void grad_cols(const GradRowsParams& p, const GradIn<MATS, DT, VEC>& in,
                                           const Raw<float, VEC> (&sc)[MATS], float xd, float (&v)[MATS][VEC],
                                           float (&sum)[2][VEC]) {
@@ -169,7 +169,7 @@ __device__ __forceinline__ void grad_cols(const GradRowsParams& p, const GradIn<
             const float s1 = sc[MATS - 1].get(i);
             const float xg = xd * (float)in.acc[0].get(i), xu = xd * (float)in.acc[MATS - 1].get(i);
             float act, dact;
-            act_value_grad(p.act, xg * s0, act, dact);
+            act_value_grad<ACT>(xg * s0, act, dact);
             const float dg = dy * (xu * s1) * dact, du = dy * act;
             v[0][i] = dg * s0;
             v[MATS - 1][i] = du * s1;
@@ -185,13 +185,17 @@ __device__ __forceinline__ void grad_cols(const GradRowsParams& p, const GradIn<
 
 // The digits of VEC values into the row's planes.  Adding 128 to each of the
 // lower digits' places turns the signed digits into the bytes of one integer,
-// off by their top bit.
+// off by their top bit.  Two planes' integers are read off the mantissa of a
+// sum with 1.5 * 2^23 (one fused multiply-add, where the conversion has a
+// quarter of its rate); three planes' are too large for that.
 template <int P, int VEC>
-__device__ __forceinline__ void store_planes(const GradRowsParams& p, int64_t t, int m, int c, int mats, float pre,
-                                             float inv, const float (&v)[VEC]) {
+__device__ __forceinline__ void store_planes(const GradRowsParams& p, int64_t t, int m, int c, int mats, float mult,
+                                             const float (&v)[VEC]) {
     int r[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) r[i] = __float2int_rn(v[i] * pre * inv) + (P == 2 ? 0x8080 : 0x808080);
+    for (int i = 0; i < VEC; ++i)
+        r[i] = P == 2 ? __float_as_int(fmaf(v[i], mult, 12582912.0f)) + (0x8080 - 0x4B400000)
+                      : __float2int_rn(v[i] * mult) + 0x808080;
     const int64_t row = mats * p.pitch;
     int8_t* o = p.planes + t * row + m * p.pitch + c;
     store_bytes<VEC, 0>(o, r, 0x80808080u);
@@ -199,27 +203,32 @@ __device__ __forceinline__ void store_planes(const GradRowsParams& p, int64_t t,
     if constexpr (P == 3) store_bytes<VEC, 2>(o + 2 * p.T * row, r, 0x80808080u);
 }
 
+// The larger magnitude; a NaN stays one (a plain maximum would drop it).
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float r;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 template <int MATS, int VEC>
-__device__ __forceinline__ void peak_of(const float (&v)[MATS][VEC], uint32_t& m) {
+__device__ __forceinline__ void peak_of(const float (&v)[MATS][VEC], float& m) {
 #pragma unroll
     for (int k = 0; k < MATS; ++k)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) m = max(m, __float_as_uint(v[k][i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < VEC; ++i) m = max_abs(m, v[k][i]);
 }
 
-// The fixed point of a row from its largest magnitude.  A row with an infinity
-// or a NaN has none: its scale is NaN and its digits are zero.  Tiny rows are
-// lifted by 2^64 first, so that D / m stays finite and m / D a normal number.
+// The fixed point of a row from its largest magnitude: the multiplier D / m of
+// its values, after a lift by 2^64 of tiny rows, so that D / m stays finite and
+// m / D a normal number.  A row with an infinity or a NaN has no fixed point: its
+// scale is NaN, whatever its digits.
 template <int P>
-__device__ __forceinline__ bool fixed_point(uint32_t m, float& pre, float& inv, RowScale& scale) {
-    const bool finite = m < kInfBits;
+__device__ __forceinline__ float fixed_point(uint32_t m, float& lift, RowScale& scale) {
     const float mx = __uint_as_float(m);
-    pre = mx < 8.673617379884035e-19f ? 1.8446744073709552e19f : 1.0f;  // 2^-60, 2^64
-    const float mp = mx * pre;
-    const bool live = finite && mp > 0.0f;
-    inv = live ? __fdiv_rn(kPlaneMax<P>, mp) : 0.0f;
-    scale = RowScale{finite ? __fdiv_rn(mp, kPlaneMax<P>) : __uint_as_float(0x7FC00000u), 1.0f / pre};
-    return live;
+    lift = mx < 8.673617379884035e-19f ? 1.8446744073709552e19f : 1.0f;  // 2^-60, 2^64
+    const float mp = mx * lift;
+    scale = RowScale{m < kInfBits ? __fdiv_rn(mp, kPlaneMax<P>) : __uint_as_float(0x7FC00000u), 1.0f / lift};
+    return m < kInfBits && mp > 0.0f ? __fdiv_rn(kPlaneMax<P>, mp) : 0.0f;
 }
 
 // A thread owns NJ groups of VEC columns; the next row's loads are in flight
@@ -265,29 +274,33 @@ __global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_grad_
         const float xd = xd_next;
         ahead(t + (int64_t)(kRowsAhead + 1) * gridDim.x);
         float v[NJ][MATS][VEC];
-        uint32_t m = 0;
+        float peak = 0.0f;
+        with_act(MATS == 2 ? p.act : MOE_ACT_SILU, [&](auto act) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            if (col(j) < p.N) {
-                grad_cols<MATS, DT, VEC>(p, in[j], sc[j], xd, v[j], sum[j]);
-                peak_of<MATS, VEC>(v[j], m);
-            }
+            for (int j = 0; j < NJ; ++j)
+                if (col(j) < p.N) {
+                    grad_cols<decltype(act)::value, MATS, DT, VEC>(p, in[j], sc[j], xd, v[j], sum[j]);
+                    peak_of<MATS, VEC>(v[j], peak);
+                }
+        });
         if (t + gridDim.x < p.T) fetch(t + gridDim.x);
-        m = block_max_bits(m, sh, buf);
-        float pre, inv;
+        float lift;
         RowScale scale;
-        const bool live = fixed_point<P>(m, pre, inv, scale);
+        const float mult = fixed_point<P>(block_max_bits(__float_as_uint(fabsf(peak)), sh, buf), lift, scale);
         if (threadIdx.x == 0) p.scale[t] = scale;
+        if (lift != 1.0f) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int k = 0; k < MATS; ++k)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) v[j][k][i] *= lift;
+        }
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
             if (col(j) < p.N)
 #pragma unroll
-                for (int k = 0; k < MATS; ++k) {
-                    if (!live)
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) v[j][k][i] = 0.0f;
-                    store_planes<P, VEC>(p, t, k, col(j), MATS, pre, inv, v[j][k]);
-                }
+                for (int k = 0; k < MATS; ++k) store_planes<P, VEC>(p, t, k, col(j), MATS, mult, v[j][k]);
     }
     float* part = p.partials + (int64_t)blockIdx.x * 2 * p.N;
 #pragma unroll
@@ -308,36 +321,35 @@ __global__ void __launch_bounds__(1024) k_grad_rows_long(const GradRowsParams p)
     pdl_wait();
     pdl_launch_dependents();
     float* part = p.partials + (int64_t)blockIdx.x * 2 * p.N;
+    auto column = [&](int64_t t, int c, float xd, float (&v)[MATS][1], float (&sum)[2][1]) {
+        GradIn<MATS, DT, 1> in;
+        Raw<float, 1> sc[MATS];
+        in.load(p, t, c);
+        for (int k = 0; k < MATS; ++k) sc[k].load(p.s[k] + c);
+        with_act(MATS == 2 ? p.act : MOE_ACT_SILU,
+                 [&](auto act) { grad_cols<decltype(act)::value, MATS, DT, 1>(p, in, sc, xd, v, sum); });
+    };
     int buf = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
         const float xd = p.xd ? p.xd[t] : 0.0f;
-        uint32_t m = 0;
+        float peak = 0.0f;
         for (int c = threadIdx.x; c < p.N; c += blockDim.x) {
-            GradIn<MATS, DT, 1> in;
             float v[MATS][1], sum[2][1];
-            Raw<float, 1> sc[MATS];
-            for (int k = 0; k < MATS; ++k) sc[k].load(p.s[k] + c);
             for (int k = 0; k < 2; ++k) sum[k][0] = t == blockIdx.x ? 0.0f : part[(int64_t)k * p.N + c];
-            in.load(p, t, c);
-            grad_cols<MATS, DT, 1>(p, in, sc, xd, v, sum);
-            peak_of<MATS, 1>(v, m);
+            column(t, c, xd, v, sum);
+            peak_of<MATS, 1>(v, peak);
             for (int k = 0; k < 2; ++k) part[(int64_t)k * p.N + c] = sum[k][0];
         }
-        m = block_max_bits(m, sh, buf);
-        float pre, inv;
+        float lift;
         RowScale scale;
-        const bool live = fixed_point<P>(m, pre, inv, scale);
+        const float mult = fixed_point<P>(block_max_bits(__float_as_uint(fabsf(peak)), sh, buf), lift, scale);
         if (threadIdx.x == 0) p.scale[t] = scale;
         for (int c = threadIdx.x; c < p.N; c += blockDim.x) {
-            GradIn<MATS, DT, 1> in;
             float v[MATS][1], sum[2][1] = {{0.0f}, {0.0f}};
-            Raw<float, 1> sc[MATS];
-            for (int k = 0; k < MATS; ++k) sc[k].load(p.s[k] + c);
-            in.load(p, t, c);
-            grad_cols<MATS, DT, 1>(p, in, sc, xd, v, sum);
+            column(t, c, xd, v, sum);
             for (int k = 0; k < MATS; ++k) {
-                if (!live) v[k][0] = 0.0f;
-                store_planes<P, 1>(p, t, k, c, MATS, pre, inv, v[k]);
+                v[k][0] *= lift;
+                store_planes<P, 1>(p, t, k, c, MATS, mult, v[k]);
             }
         }
     }
