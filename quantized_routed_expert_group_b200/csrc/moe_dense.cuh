@@ -302,15 +302,20 @@ struct GradRowsArgs {
     int8_t* planes;  // [P][T][n_mats * pitch]
     int64_t pitch;
     RowScale* scale;   // [T]
-    float* partials;   // [grid][2][N] column sums
+    float* partials;   // column sums: gated [grid][2][N]; one matrix [chunks][2][N]
+    int* done;         // one matrix: counters of the column sums' tiles
 };
 int grad_rows_grid(int T);
-// n_part: how many partial sums of each column there are.
+constexpr int kMaxDotChunks = 64;  // row chunks of one matrix's column sums
+int col_dots_tiles(int N);         // their counters, at most
+// n_part: gated, how many partial sums of each column there are.
 cudaError_t launch_grad_rows(const GradRowsArgs& a, int* n_part, cudaStream_t s);
-// The column sums (gated: ds_gate, ds_up; matmul: ds, dbias; each may be null)
-// from the partials.  Follows the gradient's product on the stream and runs
-// beside it: the partials were complete before that product began.
+// The column sums (each may be null), after the gradient's product on the
+// stream and beside it: what they read was complete before that product began.
+// gated: ds_gate and ds_up from the partials
 cudaError_t launch_col_sums(const float* partials, int n_part, int N, float* out0, float* out1, cudaStream_t s);
+// one matrix: ds and dbias from dy and acc
+cudaError_t launch_col_dots(const GradRowsArgs& a, float* ds, float* dbias, cudaStream_t s);
 
 }  // namespace dense
 }  // namespace moe

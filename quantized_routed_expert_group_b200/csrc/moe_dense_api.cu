@@ -44,7 +44,7 @@ static int check_matrix(const void* p, int dtype, int64_t ld, int cols) {
 }
 
 struct BackwardLayout {
-    size_t planes, scale, partials, total;
+    size_t planes, scale, partials, done, total;
     int64_t pitch;
 };
 
@@ -54,7 +54,9 @@ static BackwardLayout backward_layout(int n_mats, int T, int rows, int dtype) {
     L.planes = 0;
     L.scale = align256((size_t)planes_of(dtype) * T * n_mats * L.pitch);
     L.partials = L.scale + align256((size_t)T * sizeof(RowScale));
-    L.total = L.partials + align256((size_t)grad_rows_grid(T) * 2 * rows * sizeof(float));
+    const size_t parts = n_mats == 2 ? grad_rows_grid(T) : T / 32 < kMaxDotChunks ? T / 32 : kMaxDotChunks;
+    L.done = L.partials + align256(parts * 2 * rows * sizeof(float));
+    L.total = L.done + (n_mats == 2 ? 0 : align256(col_dots_tiles(rows) * sizeof(int)));
     return L;
 }
 
@@ -90,6 +92,7 @@ static int backward(int n_mats, const void* dy, int dtype, int64_t lddy, const i
     r.pitch = L.pitch;
     r.scale = reinterpret_cast<RowScale*>(ws + L.scale);
     r.partials = reinterpret_cast<float*>(ws + L.partials);
+    r.done = reinterpret_cast<int*>(ws + L.done);
     GemmArgs g{};
     for (int m = 0; m < n_mats; ++m) {
         r.s[m] = sc[m];
@@ -112,7 +115,9 @@ static int backward(int n_mats, const void* dy, int dtype, int64_t lddy, const i
     g.ldo = lddx;
     g.dtype = dtype;
     st = status_of(launch_grad_matmul(g, s));
-    if (!st && (sum0 || sum1)) st = status_of(launch_col_sums(r.partials, n_part, rows, sum0, sum1, s));
+    if (!st && (sum0 || sum1))
+        st = status_of(n_mats == 2 ? launch_col_sums(r.partials, n_part, rows, sum0, sum1, s)
+                                   : launch_col_dots(r, sum0, sum1, s));
     return st;
 }
 

@@ -21,13 +21,20 @@ __device__ __forceinline__ uint32_t block_max_bits(uint32_t m, uint32_t* sh, int
     return __reduce_max_sync(kFull, lane < nw ? sh[buf * 32 + lane] : 0u);
 }
 
+// The larger magnitude; a NaN stays one (a plain maximum would drop it).
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float r;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // ---------------------------------------------------------------------------
 // Per-token quantiser: one CTA a row.  d = amax / 127, q = round-half-away(x *
 // (1/d)), the steps of the block quantiser over the whole row.
 // Memory bound: the row is read once and kept in registers (rows up to
 // kQuantCache * VEC * blockDim elements; longer ones are read again from L2).
 // ---------------------------------------------------------------------------
-constexpr int kQuantCache = 8;
+constexpr int kQuantCache = 4;
 
 template <int DT, int VEC>
 __global__ void __launch_bounds__(512)
@@ -42,10 +49,10 @@ __global__ void __launch_bounds__(512)
     int8_t* qr = q + row * ldq;
     const int step = blockDim.x * VEC;
     Raw<T, VEC> v[kQuantCache];
-    uint32_t m = 0;
+    float pk = 0.0f;
     auto peak = [&](const Raw<T, VEC>& r) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) m = max(m, __float_as_uint(to_f32(r.get(i))) & 0x7FFFFFFFu);
+        for (int i = 0; i < VEC; ++i) pk = max_abs(pk, to_f32(r.get(i)));
     };
 #pragma unroll
     for (int j = 0; j < kQuantCache; ++j) {
@@ -60,8 +67,7 @@ __global__ void __launch_bounds__(512)
         e.load(xr + c);
         peak(e);
     }
-    m = block_max_bits(m, sh, 0);
-    const QuantScale qs = quant_scale(m);
+    const QuantScale qs = quant_scale(block_max_bits(__float_as_uint(fabsf(pk)), sh, 0));
     const float inv = qs.inv;
     if (threadIdx.x == 0) d[row] = qs.scale;
     auto put = [&](const Raw<T, VEC>& r, int c) {
@@ -93,7 +99,7 @@ static cudaError_t quantize_token(const void* x, int64_t rows, int cols, int64_t
     // many rows: small CTAs with several loads a thread in flight, so that all
     // rows of an SM are under way together; few rows: as wide as the row
     const int groups = (cols + per - 1) / per;
-    const int each = rows >= 2 * device_info().sm_count ? 6 : 1;
+    const int each = rows >= 2 * device_info().sm_count ? kQuantCache : 1;
     int threads = (groups + 32 * each - 1) / (32 * each) * 32;
     threads = threads > 512 ? 512 : threads;
     for (int64_t r = 0; r < rows; r += 1 << 30) {  // the grid's limit
@@ -117,15 +123,18 @@ cudaError_t launch_quantize_token(const void* x, int dtype, int64_t rows, int co
 }
 
 // ---------------------------------------------------------------------------
-// Gradient rows.  A CTA takes rows blockIdx.x, + gridDim.x, ...; a thread owns
-// the same columns in each of them, so it keeps their column sums in registers
-// and writes one partial sum a column and CTA, which k_col_sums adds in CTA
-// order (a fixed grid, no atomics: the sums do not depend on timing).
-//   gated:  dg = dh u act'(g), du = dh act(g);  v = dg s_g and du s_u;
-//           column sums of dg xd acc_g and du xd acc_u
-//   matmul: v = dy s;  column sums of dy xd acc and dy
-// Both matrices' values share the row's fixed point, so that their products
-// add up in one accumulator.
+// Gradient rows of one matrix: v = dy s.  One CTA a row, like the quantiser.
+// (The column sums do not need the row's fixed point: k_col_dots forms them
+// under the gradient's product, which leaves the memory idle.)
+//
+// Gradient rows of the gated block: dg = dh u act'(g), du = dh act(g); v = dg s_g
+// and du s_u; column sums of dg xd acc_g and du xd acc_u, for which the
+// derivative would have to be formed again.  A CTA takes rows blockIdx.x,
+// + gridDim.x, ...; a thread owns the same columns in each of them, so it keeps
+// their column sums in registers and writes one partial sum a column and CTA,
+// which k_col_sums adds in CTA order (a fixed grid, no atomics: the sums do not
+// depend on timing).  Both matrices' values share the row's fixed point, so that
+// their products add up in one accumulator.
 // ---------------------------------------------------------------------------
 struct GradRowsParams {
     const void* dy;
@@ -138,48 +147,41 @@ struct GradRowsParams {
     int64_t pitch;
     RowScale* scale;
     float* partials;
+    int* done;  // one matrix: counters of k_col_dots, zeroed here
     bool bulk;  // rows of dy and acc start and end on 16 bytes
 };
 constexpr int kRowsAhead = 3;
+constexpr int kMats = 2;  // gate and up
 
 // What VEC columns of a row read.
-template <int MATS, int DT, int VEC>
+template <int DT, int VEC>
 struct GradIn {
     Raw<typename Elem<DT>::T, VEC> dy;
-    Raw<int32_t, VEC> acc[MATS];
+    Raw<int32_t, VEC> acc[kMats];
     __device__ __forceinline__ void load(const GradRowsParams& p, int64_t t, int c) {
         dy.load(static_cast<const typename Elem<DT>::T*>(p.dy) + t * p.lddy + c);
-        if (MATS == 2 || p.acc) {
 #pragma unroll
-            for (int m = 0; m < MATS; ++m) acc[m].load(p.acc + ((int64_t)m * p.T + t) * p.N + c);
-        }
+        for (int m = 0; m < kMats; ++m) acc[m].load(p.acc + ((int64_t)m * p.T + t) * p.N + c);
     }
 };
 
 // Their values and column contributions.
-template <int ACT, int MATS, int DT, int VEC>
-__device__ __forceinline__ void grad_cols(const GradRowsParams& p, const GradIn<MATS, DT, VEC>& in,
-                                          const Raw<float, VEC> (&sc)[MATS], float xd, float (&v)[MATS][VEC],
+template <int ACT, int DT, int VEC>
+__device__ __forceinline__ void grad_cols(const GradRowsParams& p, const GradIn<DT, VEC>& in,
+                                          const Raw<float, VEC> (&sc)[kMats], float xd, float (&v)[kMats][VEC],
                                           float (&sum)[2][VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         const float dy = to_f32(in.dy.get(i));
-        const float s0 = sc[0].get(i);
-        if constexpr (MATS == 2) {
-            const float s1 = sc[MATS - 1].get(i);
-            const float xg = xd * (float)in.acc[0].get(i), xu = xd * (float)in.acc[MATS - 1].get(i);
-            float act, dact;
-            act_value_grad<ACT>(xg * s0, act, dact);
-            const float dg = dy * (xu * s1) * dact, du = dy * act;
-            v[0][i] = dg * s0;
-            v[MATS - 1][i] = du * s1;
-            sum[0][i] += dg * xg;
-            sum[1][i] += du * xu;
-        } else {
-            v[0][i] = dy * s0;
-            if (p.acc) sum[0][i] += dy * (xd * (float)in.acc[0].get(i));
-            sum[1][i] += dy;
-        }
+        const float s0 = sc[0].get(i), s1 = sc[1].get(i);
+        const float xg = xd * (float)in.acc[0].get(i), xu = xd * (float)in.acc[1].get(i);
+        float act, dact;
+        act_value_grad<ACT>(xg * s0, act, dact);
+        const float dg = dy * (xu * s1) * dact, du = dy * act;
+        v[0][i] = dg * s0;
+        v[1][i] = du * s1;
+        sum[0][i] += dg * xg;
+        sum[1][i] += du * xu;
     }
 }
 
@@ -203,17 +205,10 @@ __device__ __forceinline__ void store_planes(const GradRowsParams& p, int64_t t,
     if constexpr (P == 3) store_bytes<VEC, 2>(o + 2 * p.T * row, r, 0x80808080u);
 }
 
-// The larger magnitude; a NaN stays one (a plain maximum would drop it).
-__device__ __forceinline__ float max_abs(float a, float b) {
-    float r;
-    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-template <int MATS, int VEC>
-__device__ __forceinline__ void peak_of(const float (&v)[MATS][VEC], float& m) {
+template <int VEC>
+__device__ __forceinline__ void peak_of(const float (&v)[kMats][VEC], float& m) {
 #pragma unroll
-    for (int k = 0; k < MATS; ++k)
+    for (int k = 0; k < kMats; ++k)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) m = max_abs(m, v[k][i]);
 }
@@ -231,16 +226,176 @@ __device__ __forceinline__ float fixed_point(uint32_t m, float& lift, RowScale& 
     return m < kInfBits && mp > 0.0f ? __fdiv_rn(kPlaneMax<P>, mp) : 0.0f;
 }
 
-// A thread owns NJ groups of VEC columns; the next row's loads are in flight
-// while a row waits for its largest value.
-template <int MATS, int DT, int VEC, int NJ>
-__global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_grad_rows(const GradRowsParams p) {
+// Rows of one matrix.
+constexpr int kRowCache = 6;
+
+template <int DT, int VEC>
+__global__ void __launch_bounds__(512, 2) k_grad_rows(const GradRowsParams p) {
+    using T = typename Elem<DT>::T;
     constexpr int P = planes_of(DT);
     __shared__ uint32_t sh[64];
     pdl_wait();
     pdl_launch_dependents();
-    GradIn<MATS, DT, VEC> in[NJ];
-    Raw<float, VEC> sc[NJ][MATS];
+    const int64_t t = blockIdx.x;
+    if (t == 0)
+        for (int i = threadIdx.x; i < (p.N + 31) / 32; i += blockDim.x) p.done[i] = 0;
+    const T* dy = static_cast<const T*>(p.dy) + t * p.lddy;
+    const int step = blockDim.x * VEC;
+    auto value = [&](int c, float (&v)[VEC]) {
+        Raw<T, VEC> d;
+        Raw<float, VEC> s;
+        d.load(dy + c);
+        s.load(p.s[0] + c);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = to_f32(d.get(i)) * s.get(i);
+    };
+    float v[kRowCache][VEC], peak = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kRowCache; ++j) {
+        const int c = threadIdx.x * VEC + j * step;
+        if (c < p.N) value(c, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kRowCache; ++j)
+        if (threadIdx.x * VEC + j * step < p.N)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) peak = max_abs(peak, v[j][i]);
+    for (int c = threadIdx.x * VEC + kRowCache * step; c < p.N; c += step) {
+        float w[VEC];
+        value(c, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) peak = max_abs(peak, w[i]);
+    }
+    float lift;
+    RowScale scale;
+    const float mult = fixed_point<P>(block_max_bits(__float_as_uint(fabsf(peak)), sh, 0), lift, scale);
+    if (threadIdx.x == 0) p.scale[t] = scale;
+    auto put = [&](int c, float (&w)[VEC]) {
+        if (lift != 1.0f) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] *= lift;
+        }
+        store_planes<P, VEC>(p, t, 0, c, 1, mult, w);
+    };
+#pragma unroll
+    for (int j = 0; j < kRowCache; ++j) {
+        const int c = threadIdx.x * VEC + j * step;
+        if (c < p.N) put(c, v[j]);
+    }
+    for (int c = threadIdx.x * VEC + kRowCache * step; c < p.N; c += step) {
+        float w[VEC];
+        value(c, w);
+        put(c, w);
+    }
+}
+
+// ds[c] = sum_t dy xd acc, dbias[c] = sum_t dy.  A CTA takes 32 VEC columns of a
+// chunk of the rows, a row for each of its warps at a time, four of them under
+// way; its sums go to the partials, and the CTA that finishes a column tile last
+// joins the chunks' in their order, in fp64 (so the result does not depend on
+// which one that is; k_grad_rows zeroed the tiles' counters).
+// It runs under the gradient's product, which leaves the memory idle: 256
+// threads and 9 KB of shared memory fit beside a pair's CTA.  It waits for that
+// product's end last, so that whatever follows finds both done.
+constexpr int kDotsWarps = 8;
+
+struct ColDotsParams {
+    const void* dy;
+    int64_t lddy;
+    const int32_t* acc;  // null: no ds
+    const float* xd;
+    int T, N, chunks;
+    float* partials;  // [chunks][2][N]
+    int* done;        // [tiles]
+    float* ds;
+    float* dbias;
+};
+
+template <int DT, int VEC>
+__global__ void __launch_bounds__(32 * kDotsWarps, 4) k_col_dots(const ColDotsParams p) {
+    using T = typename Elem<DT>::T;
+    __shared__ float sh[kDotsWarps][2][32 * VEC];
+    __shared__ int last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tile = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+    const int c = tile * 32 * VEC + lane * VEC;
+    const int64_t r1 = (int64_t)p.T * (chunk + 1) / p.chunks;
+    float sum[2][VEC] = {};
+    if (c < p.N) {
+        const T* dy = static_cast<const T*>(p.dy) + c;
+        const int32_t* acc = p.acc + c;
+        for (int64_t t = (int64_t)p.T * chunk / p.chunks + warp; t < r1; t += 4 * kDotsWarps) {
+            Raw<T, VEC> d[4];
+            Raw<int32_t, VEC> a[4];
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t r = t + k * kDotsWarps;
+                if (r < r1) {
+                    d[k].load(dy + r * p.lddy);
+                    if (p.acc) {
+                        a[k].load(acc + r * p.N);
+                        x[k] = p.xd[r];
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (t + k * kDotsWarps < r1)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const float v = to_f32(d[k].get(i));
+                        if (p.acc) sum[0][i] += v * (x[k] * (float)a[k].get(i));
+                        sum[1][i] += v;
+                    }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sh[warp][m][lane * VEC + i] = sum[m][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * 32 * VEC; i += 32 * kDotsWarps) {
+        const int m = i / (32 * VEC), col = tile * 32 * VEC + i % (32 * VEC);
+        if (col >= p.N) continue;
+        float a = 0.0f;
+        for (int w = 0; w < kDotsWarps; ++w) a += sh[w][m][i % (32 * VEC)];
+        if (p.chunks == 1) {
+            if (float* out = m ? p.dbias : p.ds) out[col] = a;
+        } else {
+            p.partials[((int64_t)chunk * 2 + m) * p.N + col] = a;
+        }
+    }
+    if (p.chunks > 1) {
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) last = atomicAdd(&p.done[tile], 1) == p.chunks - 1;
+        __syncthreads();
+        if (last) {
+            __threadfence();
+            for (int i = threadIdx.x; i < 2 * 32 * VEC; i += 32 * kDotsWarps) {
+                const int m = i / (32 * VEC), col = tile * 32 * VEC + i % (32 * VEC);
+                float* out = m ? p.dbias : p.ds;
+                if (col >= p.N || !out) continue;
+                double a = 0.0;
+                for (int k = 0; k < p.chunks; ++k) a += (double)__ldcg(&p.partials[((int64_t)k * 2 + m) * p.N + col]);
+                out[col] = (float)a;
+            }
+        }
+    }
+    pdl_wait();
+}
+
+// A thread owns NJ groups of VEC columns; the next row's loads are in flight
+// while a row waits for its largest value.
+template <int DT, int VEC, int NJ>
+__global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_gated_rows(const GradRowsParams p) {
+    constexpr int P = planes_of(DT);
+    __shared__ uint32_t sh[64];
+    pdl_wait();
+    pdl_launch_dependents();
+    GradIn<DT, VEC> in[NJ];
+    Raw<float, VEC> sc[NJ][kMats];
     float sum[NJ][2][VEC], xd_next = 0.0f;
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
@@ -248,7 +403,7 @@ __global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_grad_
         for (int i = 0; i < VEC; ++i) sum[j][0][i] = sum[j][1][i] = 0.0f;
     auto col = [&](int j) { return (int)(threadIdx.x + j * blockDim.x) * VEC; };
     auto fetch = [&](int64_t t) {
-        if (p.xd) xd_next = p.xd[t];
+        xd_next = p.xd[t];
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
             if (col(j) < p.N) in[j].load(p, t, col(j));
@@ -258,9 +413,9 @@ __global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_grad_
         if (VEC == 1 || !p.bulk || threadIdx.x != 0 || t >= p.T) return;
         using T = typename Elem<DT>::T;
         bulk_prefetch_l2(static_cast<const T*>(p.dy) + t * p.lddy, p.N * (uint32_t)sizeof(T));
-        if (MATS == 2 || p.acc)
 #pragma unroll
-            for (int m = 0; m < MATS; ++m) bulk_prefetch_l2(p.acc + ((int64_t)m * p.T + t) * p.N, p.N * 4u);
+        for (int m = 0; m < kMats; ++m)
+            bulk_prefetch_l2(p.acc + ((int64_t)m * p.T + t) * p.N, p.N * 4u);
     };
     int buf = 0;
     fetch(blockIdx.x);
@@ -269,18 +424,18 @@ __global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_grad_
     for (int j = 0; j < NJ; ++j)
         if (col(j) < p.N)
 #pragma unroll
-            for (int m = 0; m < MATS; ++m) sc[j][m].load(p.s[m] + col(j));
+            for (int m = 0; m < kMats; ++m) sc[j][m].load(p.s[m] + col(j));
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
         const float xd = xd_next;
         ahead(t + (int64_t)(kRowsAhead + 1) * gridDim.x);
-        float v[NJ][MATS][VEC];
+        float v[NJ][kMats][VEC];
         float peak = 0.0f;
-        with_act(MATS == 2 ? p.act : MOE_ACT_SILU, [&](auto act) {
+        with_act(p.act, [&](auto act) {
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
                 if (col(j) < p.N) {
-                    grad_cols<decltype(act)::value, MATS, DT, VEC>(p, in[j], sc[j], xd, v[j], sum[j]);
-                    peak_of<MATS, VEC>(v[j], peak);
+                    grad_cols<decltype(act)::value, DT, VEC>(p, in[j], sc[j], xd, v[j], sum[j]);
+                    peak_of<VEC>(v[j], peak);
                 }
         });
         if (t + gridDim.x < p.T) fetch(t + gridDim.x);
@@ -292,7 +447,7 @@ __global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_grad_
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                for (int k = 0; k < MATS; ++k)
+                for (int k = 0; k < kMats; ++k)
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) v[j][k][i] *= lift;
         }
@@ -300,7 +455,7 @@ __global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_grad_
         for (int j = 0; j < NJ; ++j)
             if (col(j) < p.N)
 #pragma unroll
-                for (int k = 0; k < MATS; ++k) store_planes<P, VEC>(p, t, k, col(j), MATS, mult, v[j][k]);
+                for (int k = 0; k < kMats; ++k) store_planes<P, VEC>(p, t, k, col(j), kMats, mult, v[j][k]);
     }
     float* part = p.partials + (int64_t)blockIdx.x * 2 * p.N;
 #pragma unroll
@@ -314,30 +469,30 @@ __global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_grad_
 
 // Rows of any length: the values are computed twice and the column sums kept
 // in the CTA's partials.
-template <int MATS, int DT>
-__global__ void __launch_bounds__(1024) k_grad_rows_long(const GradRowsParams p) {
+template <int DT>
+__global__ void __launch_bounds__(1024) k_gated_rows_long(const GradRowsParams p) {
     constexpr int P = planes_of(DT);
     __shared__ uint32_t sh[64];
     pdl_wait();
     pdl_launch_dependents();
     float* part = p.partials + (int64_t)blockIdx.x * 2 * p.N;
-    auto column = [&](int64_t t, int c, float xd, float (&v)[MATS][1], float (&sum)[2][1]) {
-        GradIn<MATS, DT, 1> in;
-        Raw<float, 1> sc[MATS];
+    auto column = [&](int64_t t, int c, float xd, float (&v)[kMats][1], float (&sum)[2][1]) {
+        GradIn<DT, 1> in;
+        Raw<float, 1> sc[kMats];
         in.load(p, t, c);
-        for (int k = 0; k < MATS; ++k) sc[k].load(p.s[k] + c);
-        with_act(MATS == 2 ? p.act : MOE_ACT_SILU,
-                 [&](auto act) { grad_cols<decltype(act)::value, MATS, DT, 1>(p, in, sc, xd, v, sum); });
+        for (int k = 0; k < kMats; ++k) sc[k].load(p.s[k] + c);
+        with_act(p.act,
+                 [&](auto act) { grad_cols<decltype(act)::value, DT, 1>(p, in, sc, xd, v, sum); });
     };
     int buf = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
-        const float xd = p.xd ? p.xd[t] : 0.0f;
+        const float xd = p.xd[t];
         float peak = 0.0f;
         for (int c = threadIdx.x; c < p.N; c += blockDim.x) {
-            float v[MATS][1], sum[2][1];
+            float v[kMats][1], sum[2][1];
             for (int k = 0; k < 2; ++k) sum[k][0] = t == blockIdx.x ? 0.0f : part[(int64_t)k * p.N + c];
             column(t, c, xd, v, sum);
-            peak_of<MATS, 1>(v, peak);
+            peak_of<1>(v, peak);
             for (int k = 0; k < 2; ++k) part[(int64_t)k * p.N + c] = sum[k][0];
         }
         float lift;
@@ -345,11 +500,11 @@ __global__ void __launch_bounds__(1024) k_grad_rows_long(const GradRowsParams p)
         const float mult = fixed_point<P>(block_max_bits(__float_as_uint(fabsf(peak)), sh, buf), lift, scale);
         if (threadIdx.x == 0) p.scale[t] = scale;
         for (int c = threadIdx.x; c < p.N; c += blockDim.x) {
-            float v[MATS][1], sum[2][1] = {{0.0f}, {0.0f}};
+            float v[kMats][1], sum[2][1] = {{0.0f}, {0.0f}};
             column(t, c, xd, v, sum);
-            for (int k = 0; k < MATS; ++k) {
+            for (int k = 0; k < kMats; ++k) {
                 v[k][0] *= lift;
-                store_planes<P, 1>(p, t, k, c, MATS, mult, v[k]);
+                store_planes<P, 1>(p, t, k, c, kMats, mult, v[k]);
             }
         }
     }
@@ -363,7 +518,7 @@ __global__ void __launch_bounds__(256) k_col_sums(const float* __restrict__ part
                                                   float* __restrict__ out0, float* __restrict__ out1) {
     __shared__ double sh[8][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane, k = blockIdx.y;
+    const int c = (int)(blockIdx.x >> 1) * 32 + lane, k = blockIdx.x & 1;
     float* out = k ? out1 : out0;
     if (out) {
         double a = 0.0;
@@ -382,16 +537,8 @@ __global__ void __launch_bounds__(256) k_col_sums(const float* __restrict__ part
 }
 
 cudaError_t launch_col_sums(const float* partials, int n_part, int N, float* out0, float* out1, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((N + 31) / 32), 2);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_col_sums, partials, n_part, N, out0, out1);
+    const unsigned tiles = (unsigned)((N + 31) / 32);
+    return launch_dense(k_col_sums, 2 * tiles, 256, 0, 1, s, partials, n_part, N, out0, out1);
 }
 
 // CTAs of the gradient row kernel: a fixed grid (the column sums' order is the
@@ -401,12 +548,12 @@ int grad_rows_grid(int T) {
     return T < most ? T : most;
 }
 
-template <int MATS, int DT>
+template <int DT>
 static cudaError_t grad_rows(const GradRowsArgs& a, GradRowsParams p, int& grid, cudaStream_t s) {
     const size_t vb = 4 * sizeof(typename Elem<DT>::T);
     bool vec = reinterpret_cast<uintptr_t>(a.dy) % vb == 0 && a.lddy % 4 == 0 && a.N % 4 == 0 &&
                reinterpret_cast<uintptr_t>(a.acc) % 16 == 0;
-    for (int m = 0; m < MATS; ++m) vec = vec && reinterpret_cast<uintptr_t>(a.s[m]) % 16 == 0;
+    for (int m = 0; m < kMats; ++m) vec = vec && reinterpret_cast<uintptr_t>(a.s[m]) % 16 == 0;
     const int esz = (int)sizeof(typename Elem<DT>::T);
     p.bulk = vec && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && a.lddy * esz % 16 == 0 && a.N * esz % 16 == 0;
     const int groups = vec ? a.N / 4 : a.N;
@@ -415,15 +562,28 @@ static cudaError_t grad_rows(const GradRowsArgs& a, GradRowsParams p, int& grid,
     const int per = vec ? (groups <= 2 * 768 ? 2 : 4) : (groups <= 512 ? 1 : 4);
     const int threads = (groups + 32 * per - 1) / (32 * per) * 32;
     if (threads > (vec ? (per == 2 ? 768 : 512) : 1024)) {
-        return launch_dense(k_grad_rows_long<MATS, DT>, grid, 1024, 0, 1, s, p);
+        return launch_dense(k_gated_rows_long<DT>, grid, 1024, 0, 1, s, p);
     }
     const int per_sm = threads > 384 ? 1 : threads > 256 ? 2 : threads > 192 ? 3 : 4;
     if (grid > per_sm * device_info().sm_count) grid = per_sm * device_info().sm_count;
     if (vec)
-        return per == 2 ? launch_dense(k_grad_rows<MATS, DT, 4, 2>, grid, threads, 0, 1, s, p)
-                        : launch_dense(k_grad_rows<MATS, DT, 4, 4>, grid, threads, 0, 1, s, p);
-    return per == 1 ? launch_dense(k_grad_rows<MATS, DT, 1, 1>, grid, threads, 0, 1, s, p)
-                    : launch_dense(k_grad_rows<MATS, DT, 1, 4>, grid, threads, 0, 1, s, p);
+        return per == 2 ? launch_dense(k_gated_rows<DT, 4, 2>, grid, threads, 0, 1, s, p)
+                        : launch_dense(k_gated_rows<DT, 4, 4>, grid, threads, 0, 1, s, p);
+    return per == 1 ? launch_dense(k_gated_rows<DT, 1, 1>, grid, threads, 0, 1, s, p)
+                    : launch_dense(k_gated_rows<DT, 1, 4>, grid, threads, 0, 1, s, p);
+}
+
+template <int DT>
+static cudaError_t one_rows(const GradRowsArgs& a, const GradRowsParams& p, cudaStream_t s) {
+    using T = typename Elem<DT>::T;
+    const bool vec = reinterpret_cast<uintptr_t>(a.dy) % (4 * sizeof(T)) == 0 && a.lddy % 4 == 0 && a.N % 4 == 0 &&
+                     reinterpret_cast<uintptr_t>(a.s[0]) % 16 == 0;
+    const int groups = vec ? a.N / 4 : a.N;
+    const int each = a.T >= 2 * device_info().sm_count ? kRowCache : 1;
+    int threads = (groups + 32 * each - 1) / (32 * each) * 32;
+    threads = threads > 512 ? 512 : threads;
+    return vec ? launch_dense(k_grad_rows<DT, 4>, a.T, threads, 0, 1, s, p)
+               : launch_dense(k_grad_rows<DT, 1>, a.T, threads, 0, 1, s, p);
 }
 
 cudaError_t launch_grad_rows(const GradRowsArgs& a, int* n_part, cudaStream_t s) {
@@ -441,18 +601,40 @@ cudaError_t launch_grad_rows(const GradRowsArgs& a, int* n_part, cudaStream_t s)
     p.pitch = a.pitch;
     p.scale = a.scale;
     p.partials = a.partials;
-    int grid = grad_rows_grid(a.T);
-    cudaError_t e;
-    if (a.n_mats == 2)
-        e = a.dtype == MOE_F32    ? grad_rows<2, MOE_F32>(a, p, grid, s)
-            : a.dtype == MOE_BF16 ? grad_rows<2, MOE_BF16>(a, p, grid, s)
-                                  : grad_rows<2, MOE_F16>(a, p, grid, s);
-    else
-        e = a.dtype == MOE_F32    ? grad_rows<1, MOE_F32>(a, p, grid, s)
-            : a.dtype == MOE_BF16 ? grad_rows<1, MOE_BF16>(a, p, grid, s)
-                                  : grad_rows<1, MOE_F16>(a, p, grid, s);
-    *n_part = grid;
-    return e;
+    p.done = a.done;
+    *n_part = grad_rows_grid(a.T);
+    if (a.n_mats == 1)
+        return a.dtype == MOE_F32    ? one_rows<MOE_F32>(a, p, s)
+               : a.dtype == MOE_BF16 ? one_rows<MOE_BF16>(a, p, s)
+                                     : one_rows<MOE_F16>(a, p, s);
+    return a.dtype == MOE_F32    ? grad_rows<MOE_F32>(a, p, *n_part, s)
+           : a.dtype == MOE_BF16 ? grad_rows<MOE_BF16>(a, p, *n_part, s)
+                                 : grad_rows<MOE_F16>(a, p, *n_part, s);
+}
+
+int col_dots_tiles(int N) { return (N + 31) / 32; }
+
+template <int DT>
+static cudaError_t col_dots(const GradRowsArgs& a, float* ds, float* dbias, cudaStream_t s) {
+    using T = typename Elem<DT>::T;
+    const bool vec = reinterpret_cast<uintptr_t>(a.dy) % (4 * sizeof(T)) == 0 && a.lddy % 4 == 0 && a.N % 4 == 0 &&
+                     reinterpret_cast<uintptr_t>(a.acc) % 16 == 0;
+    ColDotsParams p{a.dy, a.lddy, ds ? a.acc : nullptr, a.xd, a.T, a.N, 1, a.partials, a.done, ds, dbias};
+    const int tiles = vec ? (a.N + 127) / 128 : col_dots_tiles(a.N);
+    // a CTA for each SM, but 32 rows or more for each of them
+    const int most = kMaxDotChunks < a.T / 32 ? kMaxDotChunks : a.T / 32;
+    p.chunks = device_info().sm_count / tiles;
+    p.chunks = p.chunks > most ? most : p.chunks;
+    p.chunks = p.chunks < 1 ? 1 : p.chunks;
+    const unsigned grid = (unsigned)(tiles * p.chunks);
+    return vec ? launch_dense(k_col_dots<DT, 4>, grid, 32 * kDotsWarps, 0, 1, s, p)
+               : launch_dense(k_col_dots<DT, 1>, grid, 32 * kDotsWarps, 0, 1, s, p);
+}
+
+cudaError_t launch_col_dots(const GradRowsArgs& a, float* ds, float* dbias, cudaStream_t s) {
+    return a.dtype == MOE_F32    ? col_dots<MOE_F32>(a, ds, dbias, s)
+           : a.dtype == MOE_BF16 ? col_dots<MOE_BF16>(a, ds, dbias, s)
+                                 : col_dots<MOE_F16>(a, ds, dbias, s);
 }
 
 }  // namespace dense
