@@ -372,35 +372,50 @@ _CODE_TYPES = (torch.int8, torch.uint8)
 _ROW_TYPES = tuple(_DTYPES)
 
 
+def _refuse(t, dtypes, name: str, shape, dev: int):
+    """Raises with what is wrong with an operand (the checks themselves are kept
+    short: a call of a few microseconds waits for them)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() != len(shape):
+        raise ValueError(f"{name} must be a {len(shape)}-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
+    if any(w >= 0 and w != n for w, n in zip(shape, t.shape)):
+        want = tuple("any" if w < 0 else w for w in shape)
+        raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+    if dev >= 0 and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    raise ValueError(f"{name} must be dense" if len(shape) != 2 else
+                     f"{name} must have dense rows (last stride 1) that do not overlap")
+
+
 def _matrix(t: torch.Tensor, dtypes, name: str, rows: int = -1, cols: int = -1, dev: int = -1) -> int:
     """Checks a 2-D operand (its rows, columns and device where they are given);
     returns its row stride in elements."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
-    (r, c), (ld, inner) = t.shape, t.stride()
-    if (rows >= 0 and r != rows) or (cols >= 0 and c != cols):
-        want = tuple("any" if n < 0 else n for n in (rows, cols))
-        raise ValueError(f"{name} must have shape {want}, got {(r, c)}")
-    if dev >= 0 and t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
-    if r <= 1:
-        ld = c
-    if (inner != 1 and c > 1) or ld < c:
-        raise ValueError(f"{name} must have dense rows (last stride 1) that do not overlap")
-    return ld
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 2:
+        (r, c), (ld, inner) = t.shape, t.stride()
+        if r <= 1:
+            ld = c
+        d = t.get_device()
+        if (d >= 0 and (d == dev or dev < 0) and (r == rows or rows < 0) and (c == cols or cols < 0)
+                and (inner == 1 or c <= 1) and ld >= c):
+            return ld
+    _refuse(t, dtypes, name, (rows, cols), dev)
 
 
-def _vector(t: torch.Tensor, n: int, name: str, dev: int) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a dense fp32 vector of {n} values")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+_F32 = (torch.float32,)
 
 
-def _sums(acc: torch.Tensor, shape, dev: int) -> None:
+def _vector(t: torch.Tensor, n: int, name: str, dev: int) -> int:
+    """Checks a dense fp32 vector; returns its address."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 1 or t.numel() != n
+            or t.get_device() != dev or not t.is_contiguous()):
+        _refuse(t, _F32, name, (n,), dev)
+    return t.data_ptr()
+
+
+def _sums(acc: torch.Tensor, shape, dev: int) -> int:
     if (not isinstance(acc, torch.Tensor) or acc.dtype != torch.int32 or acc.shape != shape
             or not acc.is_contiguous() or acc.get_device() != dev):
         raise ValueError(f"acc must be the contiguous int32 sums {shape} that the forward saved, on cuda:{dev}")
+    return acc.data_ptr()
 
 
 def _choice(value, table, name):
@@ -410,49 +425,35 @@ def _choice(value, table, name):
         raise ValueError(f"{name} must be one of {', '.join(str(k) for k in table)}, got {value!r}") from None
 
 
-def _addr(t: torch.Tensor | None):
-    return None if t is None else t.data_ptr()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
-    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _on(dev: int, stream, call):
-    """call(stream handle) with the call's device and stream as the current ones,
-    so that what it allocates belongs to the stream that uses it."""
+def _on(dev: int, stream):
+    """A context with the call's device and stream as the current ones, so that
+    what the call allocates belongs to the stream that uses it."""
     if stream is None:
-        if dev == _current_device():
-            return call(_raw_stream(dev))
-        with torch.cuda.device(dev):
-            return call(_raw_stream(dev))
+        return torch.cuda.device(dev)
     if stream.device.index != dev:
         raise ValueError(f"stream is on {stream.device}, the call's tensors on cuda:{dev}")
-    with torch.cuda.stream(stream):  # also makes its device the current one
-        return call(stream.cuda_stream)
+    return torch.cuda.stream(stream)  # also makes its device the current one
 
 
 def quantize_act_token(x: torch.Tensor, stream=None):
     """Rows of x [T][K] (fp32, bf16 or fp16) -> codes [T][K] int8 and scales [T]
     fp32 (see moe_quantize_act_token)."""
     ld = _matrix(x, _ROW_TYPES, "x")
+    dev = x.get_device()
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return quantize_act_token(x)
     T, K = x.shape
-
-    def call(s):
-        q = torch.empty(T, K, dtype=torch.int8, device=x.device)
-        d = torch.empty(T, dtype=torch.float32, device=x.device)
-        _check(lib().moe_quantize_act_token(x.data_ptr(), _DTYPES[x.dtype], T, K, ld, q.data_ptr(), K, d.data_ptr(),
-                                            s), "quantize_act_token")
-        return q, d
-
-    return _on(x.get_device(), stream, call)
-
-
-def _result(out, T, N, dtype, like, dev):
-    if out is None:
-        return torch.empty(T, N, dtype=dtype, device=like.device), N
-    return out, _matrix(out, (dtype,), "out", T, N, dev)
+    q = x.new_empty(T, K, dtype=torch.int8)
+    d = x.new_empty(T, dtype=torch.float32)
+    st = lib().moe_quantize_act_token(x.data_ptr(), _DTYPES[x.dtype], T, K, ld, q.data_ptr(), K, d.data_ptr(),
+                                      _raw_stream(dev))
+    _check(st, "quantize_act_token")
+    return q, d
 
 
 def int8_matmul(xq: torch.Tensor, xd: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
@@ -462,23 +463,25 @@ def int8_matmul(xq: torch.Tensor, xd: torch.Tensor, w: torch.Tensor, s: torch.Te
     [T], weight codes w [N][K] with row scales s [N] -> [T][N] of out_dtype.
     save=True also returns the int32 sums [T][N] that the backward pass reads."""
     ldx = _matrix(xq, _ACT_TYPES, "xq")
-    (T, K), dev = xq.shape, xq.get_device()
+    dev = xq.get_device()
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return int8_matmul(xq, xd, w, s, bias, out_dtype, out, save)
+    T, K = xq.shape
     ldw = _matrix(w, _CODE_TYPES, "w", -1, K, dev)
     N = w.shape[0]
-    _vector(xd, T, "xd", dev)
-    _vector(s, N, "s", dev)
-    if bias is not None:
-        _vector(bias, N, "bias", dev)
+    xd_p, s_p = _vector(xd, T, "xd", dev), _vector(s, N, "s", dev)
+    bias_p = None if bias is None else _vector(bias, N, "bias", dev)
     dt = _choice(out_dtype, _DTYPES, "out_dtype")
-
-    def call(st):
-        y, ldo = _result(out, T, N, out_dtype, xq, dev)
-        acc = torch.empty(T, N, dtype=torch.int32, device=xq.device) if save else None
-        _check(lib().moe_int8_matmul(xq.data_ptr(), ldx, xd.data_ptr(), T, w.data_ptr(), ldw, s.data_ptr(), N, K,
-                                     _addr(bias), y.data_ptr(), dt, ldo, _addr(acc), st), "int8_matmul")
-        return (y, acc) if save else y
-
-    return _on(dev, stream, call)
+    if out is None:
+        y, ldo = xq.new_empty(T, N, dtype=out_dtype), N
+    else:
+        y, ldo = out, _matrix(out, (out_dtype,), "out", T, N, dev)
+    acc = xq.new_empty(T, N, dtype=torch.int32) if save else None
+    st = lib().moe_int8_matmul(xq.data_ptr(), ldx, xd_p, T, w.data_ptr(), ldw, s_p, N, K, bias_p, y.data_ptr(), dt,
+                               ldo, acc.data_ptr() if save else None, _raw_stream(dev))
+    _check(st, "int8_matmul")
+    return (y, acc) if save else y
 
 
 def int8_matmul_backward(dy: torch.Tensor, acc: torch.Tensor | None, xd: torch.Tensor | None, w: torch.Tensor,
@@ -487,29 +490,29 @@ def int8_matmul_backward(dy: torch.Tensor, acc: torch.Tensor | None, xd: torch.T
     respect to the dequantised activations xd * xq), ds [N] and dbias [N] (fp32).
     acc=None leaves ds out (None), bias_grad=False dbias."""
     lddy = _matrix(dy, _ROW_TYPES, "dy")
-    (T, N), dev = dy.shape, dy.get_device()
+    dev = dy.get_device()
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return int8_matmul_backward(dy, acc, xd, w, s, bias_grad)
+    T, N = dy.shape
     ldw = _matrix(w, _CODE_TYPES, "w", N, -1, dev)
     K = w.shape[1]
-    _vector(s, N, "s", dev)
+    s_p = _vector(s, N, "s", dev)
+    acc_p = xd_p = ds = db = None
     if acc is not None:
-        _sums(acc, (T, N), dev)
-        _vector(xd, T, "xd", dev)
-    else:
-        xd = None
+        acc_p, xd_p = _sums(acc, (T, N), dev), _vector(xd, T, "xd", dev)
+        ds = s.new_empty(N)
+    if bias_grad:
+        db = s.new_empty(N)
     dt = _DTYPES[dy.dtype]
-
-    def call(st):
-        dx = torch.empty(T, K, dtype=dy.dtype, device=dy.device)
-        ds = torch.empty(N, dtype=torch.float32, device=dy.device) if acc is not None else None
-        db = torch.empty(N, dtype=torch.float32, device=dy.device) if bias_grad else None
-        size = lib().moe_int8_backward_workspace_bytes(1, T, N, dt)
-        ws = torch.empty(size, dtype=torch.uint8, device=dy.device)
-        _check(lib().moe_int8_matmul_backward(dy.data_ptr(), dt, lddy, _addr(acc), _addr(xd), T, w.data_ptr(), ldw,
-                                              s.data_ptr(), N, K, dx.data_ptr(), K, _addr(ds), _addr(db),
-                                              ws.data_ptr(), size, st), "int8_matmul_backward")
-        return dx, ds, db
-
-    return _on(dev, stream, call)
+    dx = dy.new_empty(T, K)
+    size = lib().moe_int8_backward_workspace_bytes(1, T, N, dt)
+    ws = w.new_empty(size, dtype=torch.uint8)
+    st = lib().moe_int8_matmul_backward(dy.data_ptr(), dt, lddy, acc_p, xd_p, T, w.data_ptr(), ldw, s_p, N, K,
+                                        dx.data_ptr(), K, None if ds is None else ds.data_ptr(),
+                                        None if db is None else db.data_ptr(), ws.data_ptr(), size, _raw_stream(dev))
+    _check(st, "int8_matmul_backward")
+    return dx, ds, db
 
 
 def gated_ffn(xq: torch.Tensor, xd: torch.Tensor, w_gate: torch.Tensor, s_gate: torch.Tensor, w_up: torch.Tensor,
@@ -520,24 +523,25 @@ def gated_ffn(xq: torch.Tensor, xd: torch.Tensor, w_gate: torch.Tensor, s_gate: 
     out_dtype.  save=True also returns the int32 sums [2][T][N] (gate, up) that
     the backward pass reads."""
     ldx = _matrix(xq, _ACT_TYPES, "xq")
-    (T, K), dev = xq.shape, xq.get_device()
+    dev = xq.get_device()
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return gated_ffn(xq, xd, w_gate, s_gate, w_up, s_up, act, out_dtype, out, save)
+    T, K = xq.shape
     ldg = _matrix(w_gate, _CODE_TYPES, "w_gate", -1, K, dev)
     N = w_gate.shape[0]
     ldu = _matrix(w_up, _CODE_TYPES, "w_up", N, K, dev)
-    _vector(xd, T, "xd", dev)
-    _vector(s_gate, N, "s_gate", dev)
-    _vector(s_up, N, "s_up", dev)
+    xd_p, sg_p, su_p = _vector(xd, T, "xd", dev), _vector(s_gate, N, "s_gate", dev), _vector(s_up, N, "s_up", dev)
     dt, ac = _choice(out_dtype, _DTYPES, "out_dtype"), _choice(act, _ACTS, "act")
-
-    def call(st):
-        h, ldo = _result(out, T, N, out_dtype, xq, dev)
-        acc = torch.empty(2, T, N, dtype=torch.int32, device=xq.device) if save else None
-        _check(lib().moe_gated_ffn(xq.data_ptr(), ldx, xd.data_ptr(), T, w_gate.data_ptr(), ldg, s_gate.data_ptr(),
-                                   w_up.data_ptr(), ldu, s_up.data_ptr(), N, K, ac, h.data_ptr(), dt, ldo, _addr(acc),
-                                   st), "gated_ffn")
-        return (h, acc) if save else h
-
-    return _on(dev, stream, call)
+    if out is None:
+        h, ldo = xq.new_empty(T, N, dtype=out_dtype), N
+    else:
+        h, ldo = out, _matrix(out, (out_dtype,), "out", T, N, dev)
+    acc = xq.new_empty(2, T, N, dtype=torch.int32) if save else None
+    st = lib().moe_gated_ffn(xq.data_ptr(), ldx, xd_p, T, w_gate.data_ptr(), ldg, sg_p, w_up.data_ptr(), ldu, su_p, N,
+                             K, ac, h.data_ptr(), dt, ldo, acc.data_ptr() if save else None, _raw_stream(dev))
+    _check(st, "gated_ffn")
+    return (h, acc) if save else h
 
 
 def gated_ffn_backward(dh: torch.Tensor, acc: torch.Tensor, xd: torch.Tensor, w_gate: torch.Tensor,
@@ -547,29 +551,32 @@ def gated_ffn_backward(dh: torch.Tensor, acc: torch.Tensor, xd: torch.Tensor, w_
     forward saved: dx [T][K] (of dh's type, with respect to the dequantised
     activations xd * xq), ds_gate [N] and ds_up [N] (fp32)."""
     lddh = _matrix(dh, _ROW_TYPES, "dh")
-    (T, N), dev = dh.shape, dh.get_device()
+    dev = dh.get_device()
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return gated_ffn_backward(dh, acc, xd, w_gate, s_gate, w_up, s_up, act)
+    T, N = dh.shape
     ldg = _matrix(w_gate, _CODE_TYPES, "w_gate", N, -1, dev)
     K = w_gate.shape[1]
     ldu = _matrix(w_up, _CODE_TYPES, "w_up", N, K, dev)
-    _sums(acc, (2, T, N), dev)
-    _vector(xd, T, "xd", dev)
-    _vector(s_gate, N, "s_gate", dev)
-    _vector(s_up, N, "s_up", dev)
+    acc_p = _sums(acc, (2, T, N), dev)
+    xd_p, sg_p, su_p = _vector(xd, T, "xd", dev), _vector(s_gate, N, "s_gate", dev), _vector(s_up, N, "s_up", dev)
     dt, ac = _DTYPES[dh.dtype], _choice(act, _ACTS, "act")
+    dx = dh.new_empty(T, K)
+    dsg, dsu = s_gate.new_empty(N), s_up.new_empty(N)
+    size = lib().moe_int8_backward_workspace_bytes(2, T, N, dt)
+    ws = w_gate.new_empty(size, dtype=torch.uint8)
+    st = lib().moe_gated_ffn_backward(dh.data_ptr(), dt, lddh, acc_p, xd_p, T, w_gate.data_ptr(), ldg, sg_p,
+                                      w_up.data_ptr(), ldu, su_p, N, K, ac, dx.data_ptr(), K, dsg.data_ptr(),
+                                      dsu.data_ptr(), ws.data_ptr(), size, _raw_stream(dev))
+    _check(st, "gated_ffn_backward")
+    return dx, dsg, dsu
 
-    def call(st):
-        dx = torch.empty(T, K, dtype=dh.dtype, device=dh.device)
-        ds = torch.empty(2, N, dtype=torch.float32, device=dh.device)
-        size = lib().moe_int8_backward_workspace_bytes(2, T, N, dt)
-        ws = torch.empty(size, dtype=torch.uint8, device=dh.device)
-        dsg, dsu = ds.unbind()
-        _check(lib().moe_gated_ffn_backward(dh.data_ptr(), dt, lddh, acc.data_ptr(), xd.data_ptr(), T,
-                                            w_gate.data_ptr(), ldg, s_gate.data_ptr(), w_up.data_ptr(), ldu,
-                                            s_up.data_ptr(), N, K, ac, dx.data_ptr(), K, dsg.data_ptr(),
-                                            dsu.data_ptr(), ws.data_ptr(), size, st), "gated_ffn_backward")
-        return dx, dsg, dsu
 
-    return _on(dev, stream, call)
+def _bank_part(t: torch.Tensor, dtype, name: str, shape, dev: int) -> int:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"bank.{name} must be a contiguous {dtype} tensor {shape} on cuda:{dev} (one int8 expert)")
+    return t.data_ptr()
 
 
 def dense_ffn(x: torch.Tensor, bank: ExpertBank, act: str = "silu", out: torch.Tensor | None = None,
@@ -578,27 +585,29 @@ def dense_ffn(x: torch.Tensor, bank: ExpertBank, act: str = "silu", out: torch.T
     packed at wbits 8): matmul(quantise(gated(quantise(x)))), x [T][hidden] fp32,
     bf16 or fp16 -> the same shape and type."""
     ldx = _matrix(x, _ROW_TYPES, "x")
-    (T, H), dev = x.shape, x.get_device()
-    I = bank.w_gate.shape[1]
-    for name, t, shape, want in (("w_gate", bank.w_gate, (1, I, H), torch.uint8),
-                                 ("w_up", bank.w_up, (1, I, H), torch.uint8),
-                                 ("w_down", bank.w_down, (1, H, I), torch.uint8),
-                                 ("s_gate", bank.s_gate, (1, I), torch.float32),
-                                 ("s_up", bank.s_up, (1, I), torch.float32),
-                                 ("s_down", bank.s_down, (1, H), torch.float32)):
-        if t.dtype != want or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-            raise ValueError(f"bank.{name} must be a contiguous {want} tensor {shape} on cuda:{dev} (one int8 expert)")
+    dev = x.get_device()
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
+            return dense_ffn(x, bank, act, out)
+    (T, H), I = x.shape, bank.w_gate.shape[1]
+    u8, f32 = torch.uint8, torch.float32
+    parts = MoeExperts(_bank_part(bank.w_gate, u8, "w_gate", (1, I, H), dev),
+                       _bank_part(bank.w_up, u8, "w_up", (1, I, H), dev),
+                       _bank_part(bank.w_down, u8, "w_down", (1, H, I), dev),
+                       _bank_part(bank.s_gate, f32, "s_gate", (1, I), dev),
+                       _bank_part(bank.s_up, f32, "s_up", (1, I), dev),
+                       _bank_part(bank.s_down, f32, "s_down", (1, H), dev))
     dt, ac = _DTYPES[x.dtype], _choice(act, _ACTS, "act")
-
-    def call(st):
-        y, ldo = _result(out, T, H, x.dtype, x, dev)
-        size = lib().moe_dense_ffn_workspace_bytes(T, H, I)
-        ws = torch.empty(size, dtype=torch.uint8, device=x.device)
-        _check(lib().moe_dense_ffn(x.data_ptr(), dt, ldx, T, H, I, ctypes.byref(bank.struct()), ac, y.data_ptr(), ldo,
-                                   ws.data_ptr(), size, st), "dense_ffn")
-        return y
-
-    return _on(dev, stream, call)
+    if out is None:
+        y, ldo = x.new_empty(T, H), H
+    else:
+        y, ldo = out, _matrix(out, (x.dtype,), "out", T, H, dev)
+    size = lib().moe_dense_ffn_workspace_bytes(T, H, I)
+    ws = x.new_empty(size, dtype=u8)
+    st = lib().moe_dense_ffn(x.data_ptr(), dt, ldx, T, H, I, ctypes.byref(parts), ac, y.data_ptr(), ldo,
+                             ws.data_ptr(), size, _raw_stream(dev))
+    _check(st, "dense_ffn")
+    return y
 
 
 def dense_device_error(stream=None) -> int:
