@@ -1246,11 +1246,13 @@ static cudaError_t allow_smem(K kernel, bool (&done)[64]) {
     return e;
 }
 
-// Clusters of `split` CTAs that run at once, with one or two CTAs on an SM (the
+// [two][split]: clusters of `split` CTAs that run at once, with one or two CTAs on an SM (the
 // GPU's clusters do not cover all of its SMs: of 148, clusters of 8 with a CTA
 // on each SM use 120).
-static int clusters_at_once(bool two, int split) {
-    static int table[64][2][9];
+using ClusterTable = int[2][9];
+
+static const ClusterTable& clusters_at_once() {
+    static ClusterTable table[64];
     static std::once_flag once[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
@@ -1276,7 +1278,7 @@ static int clusters_at_once(bool two, int split) {
                 table[dev][t][c] = n < 1 ? 1 : n;
             }
     });
-    return table[dev][two][split];
+    return table[dev];
 }
 
 struct TilePlan {
@@ -1294,6 +1296,7 @@ template <int MODE, int P>
 static TilePlan plan_tile(int T, int tiles_n, int steps) {
     constexpr int kA = MODE == kGated ? 2 : 1, kV = MODE == kGated ? 2 : P;
     const int sms = device_info().sm_count;
+    const ClusterTable& fit = clusters_at_once();
     TilePlan best{};
     double least = 1e30;
     for (int nt = 16; nt <= (P == 3 ? 64 : 128); nt *= 2) {
@@ -1312,7 +1315,7 @@ static TilePlan plan_tile(int T, int tiles_n, int steps) {
             if (split > 1 && smem < cols * 512) smem = cols * 512;
             smem += kCtlBytes + 1024;
             if (smem < 456 * tmem - 1024) smem = 456 * tmem - 1024;
-            const int at_once = clusters_at_once(smem <= 112 * 1024, split);
+            const int at_once = fit[smem <= 112 * 1024][split];
             const int64_t rounds = (tiles + at_once - 1) / at_once;
             const double ctas = (double)(tiles < at_once ? tiles : at_once) * split;
             const double share = ctas > sms ? ctas / sms : 1.0;  // CTAs that share an SM
