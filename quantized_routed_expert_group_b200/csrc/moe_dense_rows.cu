@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(32 * kDotsWarps, 4) k_col_dots(const ColDotsPa
 // A thread owns NJ groups of VEC columns; the next row's loads are in flight
 // while a row waits for its largest value.
 template <int DT, int VEC, int NJ>
-__global__ void __launch_bounds__(VEC == 1 ? 1024 : NJ == 2 ? 768 : 512) k_gated_rows(const GradRowsParams p) {
+__global__ void __launch_bounds__(VEC == 1 ? 1024 : 512) k_gated_rows(const GradRowsParams p) {
     constexpr int P = planes_of(DT);
     __shared__ uint32_t sh[64];
     pdl_wait();
@@ -542,9 +542,9 @@ cudaError_t launch_col_sums(const float* partials, int n_part, int N, float* out
 }
 
 // CTAs of the gradient row kernel: a fixed grid (the column sums' order is the
-// same from call to call), at most four an SM.
+// same from call to call), at most two an SM.
 int grad_rows_grid(int T) {
-    const int most = 4 * device_info().sm_count;
+    const int most = 2 * device_info().sm_count;
     return T < most ? T : most;
 }
 
@@ -557,14 +557,15 @@ static cudaError_t grad_rows(const GradRowsArgs& a, GradRowsParams p, int& grid,
     const int esz = (int)sizeof(typename Elem<DT>::T);
     p.bulk = vec && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 && a.lddy * esz % 16 == 0 && a.N * esz % 16 == 0;
     const int groups = vec ? a.N / 4 : a.N;
-    // two groups of four columns a thread where 768 threads suffice (85
-    // registers each), four up to 512 threads; single columns one or four
-    const int per = vec ? (groups <= 2 * 768 ? 2 : 4) : (groups <= 512 ? 1 : 4);
+    // two groups of four columns a thread, four beyond 4096 columns; single columns
+    // one or four.  Two CTAs an SM without spills beat three with them (2048
+    // columns: 123.0 against 125.8 us of the training step at 2048 tokens).
+    const int per = vec ? (groups <= 2 * 512 ? 2 : 4) : (groups <= 512 ? 1 : 4);
     const int threads = (groups + 32 * per - 1) / (32 * per) * 32;
-    if (threads > (vec ? (per == 2 ? 768 : 512) : 1024)) {
+    if (threads > (vec ? 512 : 1024)) {
         return launch_dense(k_gated_rows_long<DT>, grid, 1024, 0, 1, s, p);
     }
-    const int per_sm = threads > 384 ? 1 : threads > 256 ? 2 : threads > 192 ? 3 : 4;
+    const int per_sm = threads > 384 ? 1 : 2;
     if (grid > per_sm * device_info().sm_count) grid = per_sm * device_info().sm_count;
     if (vec)
         return per == 2 ? launch_dense(k_gated_rows<DT, 4, 2>, grid, threads, 0, 1, s, p)
