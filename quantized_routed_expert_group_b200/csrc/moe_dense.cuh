@@ -221,8 +221,21 @@ struct RowScale {
 // Launches.  Every dense kernel may start while the kernel before it on the
 // stream ends (programmatic dependent launch): it waits (pdl_wait) before it
 // touches memory that others write, and lets its own successor start once it
-// runs, so that launches and prologues of a chain overlap.
+// runs, so that launches and prologues of a chain overlap.  What a kernel reads
+// may thus have been written during its own lifetime: none of its loads is
+// marked as read-only (no __ldg, no const __restrict__), which would also let
+// the compiler move it above the wait.
 // ---------------------------------------------------------------------------
+// 16 bytes that are read once: past L1, 256 bytes at a time into L2 (volatile:
+// not to be moved above the wait).
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
+
 template <typename... P, typename... A>
 cudaError_t launch_dense(void (*kernel)(P...), unsigned grid, int threads, size_t smem, int cluster, cudaStream_t s,
                          A&&... args) {

@@ -87,18 +87,18 @@ __device__ __forceinline__ uint4 load16(const uint8_t* row, int64_t c, int64_t c
     const int64_t left = cols - c;
     if (left >= 16 && unit >= 4) {
         if (unit >= 16) {
-            u.v = __ldg(reinterpret_cast<const uint4*>(row + c));
+            u.v = *reinterpret_cast<const uint4*>(row + c);
         } else if (unit == 8) {
-            u.q[0] = __ldg(reinterpret_cast<const unsigned long long*>(row + c));
-            u.q[1] = __ldg(reinterpret_cast<const unsigned long long*>(row + c + 8));
+            u.q[0] = *reinterpret_cast<const uint64_t*>(row + c);
+            u.q[1] = *reinterpret_cast<const uint64_t*>(row + c + 8);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) u.d[i] = __ldg(reinterpret_cast<const uint32_t*>(row + c + 4 * i));
+            for (int i = 0; i < 4; ++i) u.d[i] = *reinterpret_cast<const uint32_t*>(row + c + 4 * i);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (i < left) u.b[i] = __ldg(row + c + i);
+            if (i < left) u.b[i] = row[c + i];
     }
     return u.v;
 }
@@ -172,7 +172,7 @@ __device__ __forceinline__ void load_tile_direct(uint8_t* tile, const uint8_t* b
             const uint32_t* ws = reinterpret_cast<const uint32_t*>(src - shift[k] / 8);
             const int words = left[k] ? (shift[k] / 8 + left[k] + 3) / 4 : 0;
 #pragma unroll
-            for (int i = 0; i < 5; ++i) w[k][i] = i < words ? __ldg(ws + i) : 0u;
+            for (int i = 0; i < 5; ++i) w[k][i] = i < words ? ws[i] : 0u;
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -462,9 +462,9 @@ __global__ void __launch_bounds__(kTileThreads)
     if (warp >= 2) {
         if constexpr (MODE != kGrad) {
             if (n < p.out_rows) {
-                s0 = __ldg(p.s[0] + n);
-                if constexpr (MODE == kGated) s1 = __ldg(p.s[1] + n);
-                if (MODE == kMatmul && p.bias) bias = __ldg(p.bias + n);
+                s0 = p.s[0][n];
+                if constexpr (MODE == kGated) s1 = p.s[1][n];
+                if (MODE == kMatmul && p.bias) bias = p.bias[n];
             }
         }
         if (!mbar_wait_ns(accf, 0, kWaitAllNs)) set_error(&g_dense_error, kErrTimeout);
@@ -501,9 +501,9 @@ __global__ void __launch_bounds__(kTileThreads)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (nq + k < p.out_rows) {
-                    sq[0][k] = __ldg(p.s[0] + nq + k);
-                    if constexpr (MODE == kGated) sq[1][k] = __ldg(p.s[1] + nq + k);
-                    if (MODE == kMatmul && p.bias) bq[k] = __ldg(p.bias + nq + k);
+                    sq[0][k] = p.s[0][nq + k];
+                    if constexpr (MODE == kGated) sq[1][k] = p.s[1][nq + k];
+                    if (MODE == kMatmul && p.bias) bq[k] = p.bias[nq + k];
                 }
         }
         for (int c = (int)rank + (int)split * warp; c < nv; c += (int)split * (kTileThreads / 32)) {
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_dense_few(const FewParams p) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     a[u][m][h] = c >= p.cols ? make_uint4(0, 0, 0, 0)
-                                 : FAST      ? ld_stream_v4(wr[m][h] + c)
+                                 : FAST      ? ld_once_v4(wr[m][h] + c)
                                              : load16(wr[m][h], c, p.cols, p.w_unit[m]);
         }
     };
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(32 * WARPS) k_dense_few(const FewParams p) {
                     if constexpr (QUANT)
                         b = *reinterpret_cast<const uint4*>(codes + t * p.pitch + c);
                     else
-                        b = FAST ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + t * p.ldx + c))
+                        b = FAST ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + t * p.ldx + c)
                                  : load16(static_cast<const uint8_t*>(p.x) + t * p.ldx, c, p.cols, p.x_unit);
                 }
 #pragma unroll

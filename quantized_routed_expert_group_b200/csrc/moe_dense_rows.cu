@@ -38,8 +38,8 @@ constexpr int kQuantCache = 4;
 
 template <int DT, int VEC>
 __global__ void __launch_bounds__(512)
-    k_quantize_token(const typename Elem<DT>::T* __restrict__ x, int64_t ldx, int cols, int8_t* __restrict__ q,
-                     int64_t ldq, float* __restrict__ d) {
+    k_quantize_token(const typename Elem<DT>::T* x, int64_t ldx, int cols, int8_t* q,
+                     int64_t ldq, float* d) {
     using T = typename Elem<DT>::T;
     __shared__ uint32_t sh[64];
     pdl_wait();
@@ -514,8 +514,8 @@ __global__ void __launch_bounds__(1024) k_gated_rows_long(const GradRowsParams p
 // warps adds every 8th partial in fp64, then the warps' sums are added in order.
 // It runs under the gradient's product (small CTAs, no shared memory to speak
 // of), whose end it waits for last, so that whatever follows finds both done.
-__global__ void __launch_bounds__(256) k_col_sums(const float* __restrict__ partials, int n_part, int N,
-                                                  float* __restrict__ out0, float* __restrict__ out1) {
+__global__ void __launch_bounds__(256) k_col_sums(const float* partials, int n_part, int N,
+                                                  float* out0, float* out1) {
     __shared__ double sh[8][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = (int)(blockIdx.x >> 1) * 32 + lane, k = blockIdx.x & 1;
