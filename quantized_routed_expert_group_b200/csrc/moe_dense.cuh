@@ -255,8 +255,69 @@ cudaError_t launch_dense(void (*kernel)(P...), unsigned grid, int threads, size_
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// Up to 16 bytes at any address, from the aligned words that hold them (no word
+// without one of them is read): first the loads, then the bytes, zeros past `left`.
+struct Words {
+    uint32_t w[5];
+    int shift, left;
+};
+
+__device__ __forceinline__ Words load_words(const uint8_t* src, int left) {
+    Words r;
+    r.shift = 8 * (int)(reinterpret_cast<uintptr_t>(src) & 3);
+    r.left = left;
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(src - r.shift / 8);
+    const int n = left > 0 ? (r.shift / 8 + left + 3) / 4 : 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) r.w[i] = i < n ? p[i] : 0u;
+    return r;
+}
+
+__device__ __forceinline__ uint4 join_words(const Words& r) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int keep = r.left - 4 * i;  // bytes of this word
+        o[i] = __funnelshift_r(r.w[i], r.w[i + 1], r.shift);
+        o[i] = keep >= 4 ? o[i] : keep <= 0 ? 0u : o[i] & ((1u << (8 * keep)) - 1u);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Sixteen bytes of a row from its column c on (bytes at and past `cols` read as
+// zero); unit: the widest load that suits the row.
+__device__ __forceinline__ uint4 load16(const uint8_t* row, int64_t c, int64_t cols, int unit) {
+    const int left = (int)min((int64_t)16, max((int64_t)0, cols - c));
+    if (left < 16 || unit < 4) return join_words(load_words(row + c, left));
+    if (unit == 16) return *reinterpret_cast<const uint4*>(row + c);
+    if (unit == 8) {
+        const uint2 a = *reinterpret_cast<const uint2*>(row + c), b = *reinterpret_cast<const uint2*>(row + c + 8);
+        return make_uint4(a.x, a.y, b.x, b.y);
+    }
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(row + c);
+    return make_uint4(p[0], p[1], p[2], p[3]);
+}
+
+// Bytes of the widest load that suits every row: 16, 8, 4 or 1.
+inline int unit_of(const void* p, int64_t ld) {
+    const uint64_t b = reinterpret_cast<uintptr_t>(p) | (uint64_t)ld;
+    return b % 16 == 0 ? 16 : b % 8 == 0 ? 8 : b % 4 == 0 ? 4 : 1;
+}
+
+// The device's whole shared memory for a kernel (once a device).
+template <typename K>
+cudaError_t allow_smem(K kernel, bool (&done)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, device_info().max_smem_optin);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
+
 // ---------------------------------------------------------------------------
-// The tiled product kernel (moe_dense_gemm.cu)
+// The products (moe_dense_gemm.cu, moe_dense_few.cu)
 // ---------------------------------------------------------------------------
 enum GemmMode { kMatmul = 0, kGated = 1, kGrad = 2 };
 
@@ -286,13 +347,17 @@ struct GemmArgs {
 
 cudaError_t launch_matmul(const GemmArgs& a, cudaStream_t s);
 cudaError_t launch_gated(const GemmArgs& a, cudaStream_t s);
-// The products of up to a few float tokens (rows of x with stride a.ldx, type
-// x_type), quantised inside the kernel; for operands that few_quantised_fits.
-// dependent: the kernel before it on the stream is a dense product that does not
-// write the weights, so that they may be read before it ends.
+// Up to kFewTokens tokens (launch_matmul and launch_gated go there by themselves).
+constexpr int kFewTokens = 16;
+cudaError_t launch_few_matmul(const GemmArgs& a, cudaStream_t s);
+cudaError_t launch_few_gated(const GemmArgs& a, cudaStream_t s);
+// The products of a few tokens given as floats (rows of x with stride a.ldx),
+// quantised inside the kernel; for operands that few_quantised_fits.  The second
+// follows the first on the stream: as that does not write the weights, it reads
+// them before it ends.
 bool few_quantised_fits(const GemmArgs& a, const void* x, int x_type);
-cudaError_t launch_matmul_quantised(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s);
-cudaError_t launch_gated_quantised(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s);
+cudaError_t launch_gated_quantised(const GemmArgs& a, const void* x, int x_type, cudaStream_t s);
+cudaError_t launch_matmul_quantised(const GemmArgs& a, const float* x, cudaStream_t s);
 cudaError_t launch_grad_matmul(const GemmArgs& a, cudaStream_t s);
 cudaError_t read_device_error(cudaStream_t s, int32_t* code);
 

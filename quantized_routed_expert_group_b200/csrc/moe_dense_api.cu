@@ -328,8 +328,8 @@ MOE_API int moe_dense_ffn(const void* x, int dtype, int64_t ldx, int T, int hidd
     b.dtype = dtype;
     if (few_quantised_fits(a, x, dtype) && few_quantised_fits(b, h, MOE_F32)) {
         // a few tokens: each product quantises its own input, two launches
-        st = status_of(launch_gated_quantised(a, x, dtype, false, (cudaStream_t)stream));
-        if (!st) st = status_of(launch_matmul_quantised(b, h, MOE_F32, true, (cudaStream_t)stream));
+        st = status_of(launch_gated_quantised(a, x, dtype, (cudaStream_t)stream));
+        if (!st) st = status_of(launch_matmul_quantised(b, h, (cudaStream_t)stream));
         return st;
     }
     st = moe_quantize_act_token(x, dtype, T, hidden, ldx, xq, L.ldx, xd, stream);

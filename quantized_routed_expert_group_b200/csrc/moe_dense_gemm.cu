@@ -1,13 +1,15 @@
 // moe_dense_gemm.cu -- the tensor-core products of the dense int8 operators.
 //
-// One kernel for three products, with the weights as the MMA's 128-row operand
-// and the tokens as its columns:
+// Three products, each exact in int32 over its whole contraction:
 //   matmul  acc[t, n] = sum_k xq[t, k] w[n, k]
 //   gated   the same for two matrices at once, joined by act(g) u
 //   grad    dx[t, k]  = sum_n v[t, n] w[n, k] over one or two matrices, v in
 //           fixed-point planes; the weight tile is read as it lies in memory
 //           (rows of w are the contraction there), so the MMA takes it in its
 //           row-transposed form and nothing is ever transposed in memory
+// and two kernels: k_dense_tile (a CTA a tile, or a cluster that splits the
+// contraction) and k_dense_pair (persistent pairs of CTAs) for larger batches.
+// Up to 16 tokens the forward products stream the weights in moe_dense_few.cu.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -75,34 +77,6 @@ __device__ __forceinline__ uint32_t idesc_tile(int n) {
     return idesc_i8(n) | (MODE == kGrad ? 1u << 15 : 0u);  // A transposed
 }
 
-// Sixteen bytes of a row from its column c on (bytes at and past `cols` read as zero).
-__device__ __forceinline__ uint4 load16(const uint8_t* row, int64_t c, int64_t cols, int unit) {
-    union {
-        uint4 v;
-        uint64_t q[2];
-        uint32_t d[4];
-        uint8_t b[16];
-    } u;
-    u.v = make_uint4(0, 0, 0, 0);
-    const int64_t left = cols - c;
-    if (left >= 16 && unit >= 4) {
-        if (unit >= 16) {
-            u.v = *reinterpret_cast<const uint4*>(row + c);
-        } else if (unit == 8) {
-            u.q[0] = *reinterpret_cast<const uint64_t*>(row + c);
-            u.q[1] = *reinterpret_cast<const uint64_t*>(row + c + 8);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) u.d[i] = *reinterpret_cast<const uint32_t*>(row + c + 4 * i);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < left) u.b[i] = row[c + i];
-    }
-    return u.v;
-}
-
 // Asynchronous copy of up to BYTES bytes (n of them; the rest is zero-filled).
 template <int BYTES>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int n) {
@@ -159,33 +133,17 @@ __device__ __forceinline__ void load_tile_direct(uint8_t* tile, const uint8_t* b
         return;
     }
     for (int r0 = tid >> 3; r0 < n; r0 += 64) {
-        uint32_t w[4][5];
-        int shift[4], left[4];
+        Words w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int r = r0 + 16 * k;
             const bool ok = r < n && row0 + r < rows;
-            const uint8_t* src = base + (ok ? row0 + r : 0) * ld + col;
-            shift[k] = 8 * (int)(reinterpret_cast<uintptr_t>(src) & 3);
-            left[k] = ok ? in_row : 0;
-            // the aligned words that hold the chunk's bytes inside the row
-            const uint32_t* ws = reinterpret_cast<const uint32_t*>(src - shift[k] / 8);
-            const int words = left[k] ? (shift[k] / 8 + left[k] + 3) / 4 : 0;
-#pragma unroll
-            for (int i = 0; i < 5; ++i) w[k][i] = i < words ? ws[i] : 0u;
+            w[k] = load_words(base + (ok ? row0 + r : 0) * ld + col, ok ? in_row : 0);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int r = r0 + 16 * k;
-            if (r >= n) break;
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                o[i] = __funnelshift_r(w[k][i], w[k][i + 1], shift[k]);
-                const int keep = left[k] - 4 * i;  // bytes of this word inside the row
-                o[i] = keep >= 4 ? o[i] : keep <= 0 ? 0u : o[i] & ((1u << (8 * keep)) - 1u);
-            }
-            *reinterpret_cast<uint4*>(tile + sw128_chunk(r, c)) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (r < n) *reinterpret_cast<uint4*>(tile + sw128_chunk(r, c)) = join_words(w[k]);
         }
     }
 }
@@ -559,219 +517,6 @@ __global__ void __launch_bounds__(kTileThreads)
             }
         }
         cluster_sync_all();  // the peers have read this CTA's sums
-    }
-}
-
-// ---------------------------------------------------------------------------
-// A few tokens: the weights' stream
-// ---------------------------------------------------------------------------
-// With up to 16 tokens the products read every weight once and little else, so
-// what counts is bytes in flight and few instructions for each.  A CTA takes 16
-// rows (gated: of both matrices), its warps every kWarps-th 64-byte column of
-// them: a lane loads 16 bytes of two rows straight into the A fragments of two
-// m16n8k32 products (the order of k inside a fragment is free as long as the
-// tokens' B fragments use the same), with kUnroll columns under way.  Up to 8
-// tokens cost what one does.  The warps' integer sums meet in shared memory.
-// (The tcgen05 kernels need a tile of 128 rows in shared memory first; here that
-// detour costs more than the products.)
-//
-// With QUANT the tokens come as floats: every CTA quantises all of them into
-// shared memory, with the arithmetic of k_quantize_token, while its first
-// weights are under way; that saves a launch and a trip through L2.
-constexpr int kFewTokens = 16;
-constexpr int kFewRows = 16;
-
-struct FewParams {
-    const uint8_t* w[kMaxMats];
-    int64_t ldw[kMaxMats];
-    const void* x;
-    int64_t ldx;
-    const float* xd;
-    const float* s[kMaxMats];
-    const float* bias;
-    void* out;
-    int64_t ldo;
-    int32_t* acc;
-    int T, rows, cols;
-    int pitch;   // QUANT: bytes of a token's codes in shared memory
-    int act, dtype;
-    int w_unit[kMaxMats], x_unit;
-    bool dependent;  // the kernel before this one does not write the weights
-};
-
-__device__ __forceinline__ void mma_16832(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// XT: int8_t codes, or the type of tokens to quantise.  NB: blocks of 8 tokens.
-// FAST: weight rows (and codes) on the 16-byte grid and cols a multiple of 16.
-template <int MODE, int NB, typename XT, bool FAST, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) k_dense_few(const FewParams p) {
-    constexpr int M = MODE == kGated ? 2 : 1;
-    constexpr bool QUANT = sizeof(XT) > 1;
-    constexpr int kUnroll = FAST ? (M == 2 ? 4 : 6) : 1;
-    extern __shared__ __align__(16) uint8_t few_smem[];
-    int* red = reinterpret_cast<int*>(few_smem);  // [WARPS][M][NB][128]
-    uint32_t* peak = reinterpret_cast<uint32_t*>(few_smem + WARPS * M * NB * 512);  // QUANT: [8 NB]
-    uint8_t* codes = reinterpret_cast<uint8_t*>(peak + 8 * NB);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int64_t row0 = (int64_t)blockIdx.x * kFewRows;
-    const int nch = (p.cols + 63) / 64;
-    const uint8_t* wr[M][2];
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) wr[m][h] = p.w[m] + min(row0 + g + 8 * h, (int64_t)p.rows - 1) * p.ldw[m];
-    uint4 a[kUnroll][M][2];
-    auto load_w = [&](int ch) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int c = (ch + u * WARPS) * 64 + 16 * q;
-#pragma unroll
-            for (int m = 0; m < M; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    a[u][m][h] = c >= p.cols ? make_uint4(0, 0, 0, 0)
-                                 : FAST      ? ld_once_v4(wr[m][h] + c)
-                                             : load16(wr[m][h], c, p.cols, p.w_unit[m]);
-        }
-    };
-    if (!p.dependent) pdl_wait();
-    load_w(warp);
-    if (p.dependent) pdl_wait();
-    pdl_launch_dependents();
-    if constexpr (QUANT) {
-        if (threadIdx.x < 8 * NB) peak[threadIdx.x] = 0;
-        __syncthreads();
-        // `per` warps a token (one warp takes every WARPS-th token where there are
-        // more): its vectors loaded together and kept for the second pass
-        constexpr int V = 16 / (int)sizeof(XT), kKeep = 8;
-        const int per = max(1, WARPS / p.T), sub = warp % per;
-        const XT* x = static_cast<const XT*>(p.x);
-        Raw<XT, V> e[kKeep];
-        const int c0 = V * (lane + 32 * sub), step = V * 32 * per;
-        auto peak_of = [&](const Raw<XT, V>& r, uint32_t m) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(to_f32(r.get(i))) & 0x7FFFFFFFu);
-            return m;
-        };
-        auto scan = [&](int t) {
-            const XT* xr = x + t * p.ldx;
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < kKeep; ++i)
-                if (c0 + i * step < p.cols) e[i].load(xr + c0 + i * step);
-#pragma unroll
-            for (int i = 0; i < kKeep; ++i)
-                if (c0 + i * step < p.cols) m = peak_of(e[i], m);
-            for (int c = c0 + kKeep * step; c < p.cols; c += step) {
-                Raw<XT, V> r;
-                r.load(xr + c);
-                m = peak_of(r, m);
-            }
-            return __reduce_max_sync(kFull, m);
-        };
-        auto put = [&](int t, uint32_t m) {
-            const XT* xr = x + t * p.ldx;
-            int8_t* o = reinterpret_cast<int8_t*>(codes) + t * p.pitch;
-            const float inv = quant_scale(m).inv;
-            auto one = [&](const Raw<XT, V>& r, int c) {
-                int q8[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) q8[i] = round_away(__fmul_rn(to_f32(r.get(i)), inv));
-                store_bytes<V, 0>(o + c, q8, 0u);
-            };
-#pragma unroll
-            for (int i = 0; i < kKeep; ++i)
-                if (c0 + i * step < p.cols) one(e[i], c0 + i * step);
-            for (int c = c0 + kKeep * step; c < p.cols; c += step) {
-                Raw<XT, V> r;
-                r.load(xr + c);
-                one(r, c);
-            }
-        };
-        if (per == 1) {
-            for (int t = warp; t < p.T; t += WARPS) {
-                const uint32_t m = scan(t);
-                if (lane == 0) peak[t] = m;
-                put(t, m);
-            }
-        } else {
-            const int t = warp / per;
-            if (t < p.T) {
-                const uint32_t m = scan(t);
-                if (lane == 0) atomicMax(&peak[t], m);
-            }
-            __syncthreads();
-            if (t < p.T) put(t, peak[t]);
-        }
-        __syncthreads();
-    }
-    int acc[M][NB][4];
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][n][i] = 0;
-    for (int ch = warp; ch < nch; ch += kUnroll * WARPS) {
-        if (ch > warp) load_w(ch);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int c = (ch + u * WARPS) * 64 + 16 * q;
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                const int t = 8 * n + g;
-                uint4 b = make_uint4(0, 0, 0, 0);
-                if (t < p.T && c < p.cols) {
-                    if constexpr (QUANT)
-                        b = *reinterpret_cast<const uint4*>(codes + t * p.pitch + c);
-                    else
-                        b = FAST ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + t * p.ldx + c)
-                                 : load16(static_cast<const uint8_t*>(p.x) + t * p.ldx, c, p.cols, p.x_unit);
-                }
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const uint4 lo = a[u][m][0], hi = a[u][m][1];
-                    mma_16832(acc[m][n], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-                    mma_16832(acc[m][n], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < M; ++m)
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)  // [token][row]
-                red[((warp * M + m) * NB + n) * 128 + (2 * q + (i & 1)) * 16 + g + 8 * (i >> 1)] = acc[m][n][i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.T * kFewRows; i += 32 * WARPS) {
-        const int t = i / kFewRows;
-        const int64_t row = row0 + i % kFewRows;
-        if (row >= p.rows) continue;
-        int v[M];
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            v[m] = 0;
-            for (int k = 0; k < WARPS; ++k) v[m] += red[(k * M + m) * NB * 128 + i];
-            if (p.acc) p.acc[((int64_t)m * p.T + t) * p.rows + row] = v[m];
-        }
-        const float xd = QUANT ? quant_scale(peak[t]).scale : p.xd[t];
-        float y = (float)v[0] * (xd * p.s[0][row]);
-        if constexpr (MODE == kGated)
-            with_act(p.act, [&](auto act) {
-                y = act_value<decltype(act)::value>(y) * ((float)v[M - 1] * (xd * p.s[M - 1][row]));
-            });
-        else if (p.bias)
-            y += p.bias[row];
-        store_elem(p.out, t * p.ldo + row, p.dtype, y);
     }
 }
 
@@ -1230,22 +975,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-static int unit_of(const void* p, int64_t ld) {
-    const uint64_t b = reinterpret_cast<uintptr_t>(p) | (uint64_t)ld;
-    return b % 16 == 0 ? 16 : b % 8 == 0 ? 8 : b % 4 == 0 ? 4 : 1;
-}
-
-template <typename K>
-static cudaError_t allow_smem(K kernel, bool (&done)[64]) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, device_info().max_smem_optin);
-    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
-    return e;
-}
-
 // [two][split]: clusters of `split` CTAs that run at once, with one or two CTAs on an SM (the
 // GPU's clusters do not cover all of its SMs: of 148, clusters of 8 with a CTA
 // on each SM use 120).
@@ -1500,68 +1229,6 @@ static bool tma_operands(const GemmArgs& a) {
     return ok;
 }
 
-// x_type: -1 for codes, else the element type of tokens to quantise.
-template <int MODE>
-static cudaError_t run_few(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s) {
-    FewParams p{};
-    bool fast = a.cols % 16 == 0;
-    for (int m = 0; m < a.n_mats; ++m) {
-        p.w[m] = a.w[m];
-        p.ldw[m] = a.ldw[m];
-        p.s[m] = a.s[m];
-        p.w_unit[m] = unit_of(a.w[m], a.ldw[m]);
-        fast = fast && p.w_unit[m] == 16;
-    }
-    p.x = x;
-    p.ldx = a.ldx;
-    p.x_unit = unit_of(x, a.ldx);
-    if (x_type < 0) fast = fast && p.x_unit == 16;
-    p.xd = a.xd;
-    p.bias = a.bias;
-    p.out = a.out;
-    p.ldo = a.ldo;
-    p.acc = a.acc;
-    p.T = a.T;
-    p.rows = a.rows;
-    p.cols = a.cols;
-    p.act = a.act;
-    p.dtype = a.dtype;
-    p.dependent = dependent;
-    p.pitch = (a.cols + 127) / 128 * 128 + 64;  // two tokens' 64 bytes fall on different banks
-    const unsigned grid = (unsigned)((a.rows + (int64_t)kFewRows - 1) / kFewRows);
-    auto go = [&](auto nb, auto type, auto is_fast, auto warps) {
-        using XT = decltype(type);
-        constexpr int NB = decltype(nb)::value, WARPS = decltype(warps)::value;
-        auto* kernel = k_dense_few<MODE, NB, XT, decltype(is_fast)::value, WARPS>;
-        static bool attr_done[64];
-        cudaError_t e = allow_smem(kernel, attr_done);
-        if (e != cudaSuccess) return e;
-        const size_t smem = WARPS * (MODE == kGated ? 2 : 1) * NB * 512 + (x_type < 0 ? 0 : 32 * NB + (size_t)a.T * p.pitch);
-        return launch_dense(kernel, grid, 32 * WARPS, smem, 1, s, p);
-    };
-    using std::integral_constant;
-    // 16 warps a CTA where the rows give the SMs less than two CTAs each
-    auto by_size = [&](auto type) {
-        auto by_fast = [&](auto is_fast) {
-            auto by_warps = [&](auto nb) {
-                return (int64_t)grid < 2 * (int64_t)device_info().sm_count
-                           ? go(nb, type, is_fast, integral_constant<int, 16>())
-                           : go(nb, type, is_fast, integral_constant<int, 8>());
-            };
-            return a.T <= 8 ? by_warps(integral_constant<int, 1>()) : by_warps(integral_constant<int, 2>());
-        };
-        if constexpr (sizeof(type) > 1)
-            return by_fast(integral_constant<bool, true>());
-        else
-            return fast ? by_fast(integral_constant<bool, true>()) : by_fast(integral_constant<bool, false>());
-    };
-    if (x_type < 0) return by_size(int8_t());
-    if (x_type == MOE_F32) return by_size(float());
-    if (x_type == MOE_BF16) return by_size(__nv_bfloat16());
-    return by_size(__half());
-}
-
-
 // Single CTAs or pairs, by their estimates (within 20 % of the better one over 17
 // to 4096 tokens of five layer shapes; below 64 tokens a pair's rows stay empty).
 template <int MODE, int P, typename OT>
@@ -1578,7 +1245,7 @@ static cudaError_t run_product(const GemmArgs& a, cudaStream_t s) {
 
 template <int MODE>
 static cudaError_t run_forward(const GemmArgs& a, cudaStream_t s) {
-    if (a.T <= kFewTokens) return run_few<MODE>(a, a.x, -1, false, s);
+    if (a.T <= kFewTokens) return MODE == kGated ? launch_few_gated(a, s) : launch_few_matmul(a, s);
     return a.dtype == MOE_F32    ? run_product<MODE, 1, float>(a, s)
            : a.dtype == MOE_BF16 ? run_product<MODE, 1, __nv_bfloat16>(a, s)
                                  : run_product<MODE, 1, __half>(a, s);
@@ -1587,21 +1254,6 @@ static cudaError_t run_forward(const GemmArgs& a, cudaStream_t s) {
 cudaError_t launch_matmul(const GemmArgs& a, cudaStream_t s) { return run_forward<kMatmul>(a, s); }
 
 cudaError_t launch_gated(const GemmArgs& a, cudaStream_t s) { return run_forward<kGated>(a, s); }
-
-bool few_quantised_fits(const GemmArgs& a, const void* x, int x_type) {
-    bool ok = a.T <= kFewTokens && a.cols % 16 == 0 && (int64_t)a.T * a.cols <= 96 * 1024 &&
-              unit_of(x, a.ldx * (x_type == MOE_F32 ? 4 : 2)) == 16;
-    for (int m = 0; m < a.n_mats; ++m) ok = ok && unit_of(a.w[m], a.ldw[m]) == 16;
-    return ok;
-}
-
-cudaError_t launch_matmul_quantised(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s) {
-    return run_few<kMatmul>(a, x, x_type, dependent, s);
-}
-
-cudaError_t launch_gated_quantised(const GemmArgs& a, const void* x, int x_type, bool dependent, cudaStream_t s) {
-    return run_few<kGated>(a, x, x_type, dependent, s);
-}
 
 cudaError_t launch_grad_matmul(const GemmArgs& a, cudaStream_t s) {
     return a.dtype == MOE_F32    ? run_product<kGrad, planes_of(MOE_F32), float>(a, s)
