@@ -14,6 +14,12 @@
 // With QUANT the tokens come as floats: every CTA quantises all of them into
 // shared memory, with the arithmetic of k_quantize_token, while its first
 // weights are under way; that saves a launch and a trip through L2.
+//
+// Bound by the weights' way from L2 and HBM, and by the launch.  Three CTAs of 8
+// warps an SM where there are rows for them (16 tokens through 2048 x 6144: 3.9
+// us, against 6.6 us with one), one CTA of 16 warps otherwise (one token through
+// 6144 x 2048: 2.8 us, 4.5 TB/s; the gated block 7.0 us, 3.6 TB/s, with weights
+// partly out of HBM).
 #include <type_traits>
 
 #include "moe_dense.cuh"
@@ -55,11 +61,11 @@ __device__ __forceinline__ void mma_16832(int (&c)[4], uint32_t a0, uint32_t a1,
 // XT: int8_t codes, or the type of tokens to quantise.  NB: blocks of 8 tokens.
 // FAST: weight rows (and codes) on the 16-byte grid and cols a multiple of 16.
 template <int MODE, int NB, typename XT, bool FAST, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, sizeof(XT) > 1 && WARPS == 8 && MODE == kMatmul ? 3 : 1)
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? (MODE == kMatmul ? 3 : 2) : 1)
     k_dense_few(const FewParams p) {
     constexpr int M = MODE == kGated ? 2 : 1;
     constexpr bool QUANT = sizeof(XT) > 1;
-    constexpr int kUnroll = !FAST ? 2 : M == 2 || QUANT ? 4 : 6;
+    constexpr int kUnroll = !FAST ? 2 : M == 2 || QUANT || WARPS == 8 ? 4 : 6;
     extern __shared__ __align__(16) uint8_t few_smem[];
     int* red = reinterpret_cast<int*>(few_smem);  // [WARPS][M][NB][128]
     uint32_t* peak = reinterpret_cast<uint32_t*>(few_smem + WARPS * M * NB * 512);  // QUANT: [8 NB]
