@@ -211,6 +211,18 @@ constexpr int planes_of(int dtype) { return dtype == MOE_F32 ? 3 : 2; }
 template <int P>
 constexpr float kPlaneMax = P == 2 ? 32639.0f : 8355600.0f;
 
+// The planes of 16 tokens lie together, [T / 16][P][16] rows, so that a tile's
+// tokens are one box of memory whatever P is.
+constexpr int kPlaneGroup = 16;
+inline int64_t plane_rows(int planes, int64_t T) {
+    return (T + kPlaneGroup - 1) / kPlaneGroup * kPlaneGroup * planes;
+}
+// Row of token t's first plane (the others follow kPlaneGroup rows apart).
+template <int P>
+__device__ __forceinline__ int64_t plane_row(int64_t t) {
+    return t / kPlaneGroup * (P * kPlaneGroup) + t % kPlaneGroup;
+}
+
 // A row scale: value = integer * a * b (b a power of two that keeps a normal
 // when the row is tiny).
 struct RowScale {
@@ -327,12 +339,11 @@ struct GemmArgs {
     int64_t ldw[kMaxMats];
     int n_mats;
     int rows, cols;
-    // forward: codes [T][cols], row stride ldx.  gradient: planes
-    // [planes][T][ldx], matrix m's part at byte m * mat_pitch of a row
+    // forward: codes [T][cols], row stride ldx.  gradient: rows of planes (see
+    // plane_row) of ldx bytes, matrix m's part at byte m * mat_pitch
     const int8_t* x;
     int64_t ldx;
     int T;
-    int planes;
     int64_t mat_pitch;
     const float* xd;         // forward: token scales
     const float* s[kMaxMats];  // forward: row scales
@@ -377,7 +388,7 @@ struct GradRowsArgs {
     int n_mats;
     int T, N;
     int act;
-    int8_t* planes;  // [P][T][n_mats * pitch]
+    int8_t* planes;  // [plane_rows(P, T)][n_mats * pitch]
     int64_t pitch;
     RowScale* scale;   // [T]
     float* partials;   // column sums: gated [grid][2][N]; one matrix [chunks][2][N]

@@ -52,7 +52,7 @@ static BackwardLayout backward_layout(int n_mats, int T, int rows, int dtype) {
     BackwardLayout L;
     L.pitch = ((int64_t)rows + 127) / 128 * 128;
     L.planes = 0;
-    L.scale = align256((size_t)planes_of(dtype) * T * n_mats * L.pitch);
+    L.scale = align256((size_t)plane_rows(planes_of(dtype), T) * n_mats * L.pitch);
     L.partials = L.scale + align256((size_t)T * sizeof(RowScale));
     const size_t parts = n_mats == 2 ? grad_rows_grid(T) : T / 32 < kMaxDotChunks ? T / 32 : kMaxDotChunks;
     L.done = L.partials + align256(parts * 2 * rows * sizeof(float));
@@ -61,7 +61,6 @@ static BackwardLayout backward_layout(int n_mats, int T, int rows, int dtype) {
 }
 
 static int forward(GemmArgs& a, bool gated, cudaStream_t s) {
-    a.planes = 1;
     return status_of(gated ? launch_gated(a, s) : launch_matmul(a, s));
 }
 
@@ -108,7 +107,6 @@ static int backward(int n_mats, const void* dy, int dtype, int64_t lddy, const i
     g.x = r.planes;
     g.ldx = n_mats * L.pitch;
     g.T = T;
-    g.planes = planes_of(dtype);
     g.mat_pitch = L.pitch;
     g.gscale = r.scale;
     g.out = dx;

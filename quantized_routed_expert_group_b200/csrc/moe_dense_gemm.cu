@@ -44,7 +44,7 @@ struct TileParams {
     int64_t ldw[kMaxMats];
     const uint8_t* x;
     int64_t ldx;
-    int64_t mat_pitch;
+    int64_t mat_pitch, x_rows;
     const float* xd;
     const float* s[kMaxMats];
     const float* bias;
@@ -169,6 +169,14 @@ __device__ __forceinline__ int4 ld_peer(const int32_t* p, uint32_t rank) {
 template <int N>
 __device__ __forceinline__ uint32_t (&as_words(int (&v)[N]))[N] {
     return reinterpret_cast<uint32_t(&)[N]>(v);
+}
+
+// Accumulator column of sum i of a tile's token c (a multiple of 16; the next 15
+// follow): the gradient's planes alternate every 16 tokens, the gated block's
+// two projections lie nt apart.
+template <int MODE, int P>
+__device__ __forceinline__ int sum_col(int i, int c, int nt) {
+    return MODE == kGrad ? c * P + kPlaneGroup * i : i * nt + c;
 }
 
 // Where a product's results go, for lanes that are channels.
@@ -314,10 +322,7 @@ __global__ void __launch_bounds__(kTileThreads)
                 if constexpr (MODE == kGrad) {
                     const int m = ks / p.k_steps, k = (ks - m * p.k_steps) * kStageK;
                     tma_load_2d(st, m ? &wmap1 : &wmap0, n0, k, &full[s]);
-#pragma unroll
-                    for (int i = 0; i < P; ++i)
-                        tma_load_2d(st + kATile + i * p.nt * kStageK, &xmap, (int)(m * p.mat_pitch) + k,
-                                    (int)((int64_t)i * p.T + t0), &full[s]);
+                    tma_load_2d(st + kATile, &xmap, (int)(m * p.mat_pitch) + k, (int)t0 * P, &full[s]);
                 } else {
                     tma_load_2d(st, &wmap0, ks * kStageK, n0, &full[s]);
                     if constexpr (MODE == kGated) tma_load_2d(st + kATile, &wmap1, ks * kStageK, n0, &full[s]);
@@ -388,15 +393,13 @@ __global__ void __launch_bounds__(kTileThreads)
                 if constexpr (MODE == kGrad) {
                     const int m = ks / p.k_steps, k = (ks - m * p.k_steps) * kStageK;
                     load_tile_direct(st, p.w[m], p.ldw[m], p.rows, p.cols, k, n0, kTileRows, p.w_unit[m], tid);
-                    for (int i = 0; i < P; ++i)
-                        load_tile_direct(st + kATile + i * p.nt * kStageK,
-                                         p.x + (int64_t)i * p.T * p.ldx + m * p.mat_pitch, p.ldx, p.T, p.rows, t0, k,
-                                         p.nt, p.x_unit, tid);
+                    load_tile_direct(st + kATile, p.x + m * p.mat_pitch, p.ldx, p.x_rows, p.rows, t0 * P, k, P * p.nt,
+                                     p.x_unit, tid);
                 } else {
                     for (int m = 0; m < kA; ++m)
                         load_tile_direct(st + m * kATile, p.w[m], p.ldw[m], p.rows, p.cols, n0, (int64_t)ks * kStageK,
                                          kTileRows, p.w_unit[m], tid);
-                    load_tile_direct(st + kA * kATile, p.x, p.ldx, p.T, p.cols, t0, (int64_t)ks * kStageK, p.nt,
+                    load_tile_direct(st + kA * kATile, p.x, p.ldx, p.x_rows, p.cols, t0, (int64_t)ks * kStageK, p.nt,
                                      p.x_unit, tid);
                 }
             }
@@ -431,13 +434,13 @@ __global__ void __launch_bounds__(kTileThreads)
         for (int c = 0; c < nv; c += 16) {
             int r[kV][16];
 #pragma unroll
-            for (int i = 0; i < kV; ++i) tmem_ld16(tl + i * p.nt + c, as_words(r[i]));
+            for (int i = 0; i < kV; ++i) tmem_ld16(tl + sum_col<MODE, P>(i, c, p.nt), as_words(r[i]));
             tmem_wait_ld();
             if (split > 1) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
 #pragma unroll
-                    for (int i = 0; i < kV; ++i) part[(i * p.nt + c + j) * 128 + ch] = r[i][j];
+                    for (int i = 0; i < kV; ++i) part[(sum_col<MODE, P>(i, c, p.nt) + j) * 128 + ch] = r[i][j];
             } else if (n < p.out_rows) {
                 emit_channel<MODE, P, OT, 16>(co, r, t0 + c, n, nv - c, tok + c, s0, s1, bias);
             }
@@ -470,7 +473,7 @@ __global__ void __launch_bounds__(kTileThreads)
             for (uint32_t q = 0; q < 8; ++q)
 #pragma unroll
                 for (int i = 0; i < kV; ++i)
-                    w[q][i] = q < split ? ld_peer(&part[(i * p.nt + c) * 128 + 4 * lane], q) : make_int4(0, 0, 0, 0);
+                    w[q][i] = q < split ? ld_peer(&part[(sum_col<MODE, P>(i, c & ~15, p.nt) + (c & 15)) * 128 + 4 * lane], q) : make_int4(0, 0, 0, 0);
             int v[kV][4];
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
@@ -770,6 +773,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const PairUnit u = pair_unit(p, unit);
                 const int r0 = (int)u.r0 + 128 * rank;
                 const CUtensorMap* bm = u.part ? bs : bw;
+                // this CTA's half of the columns: token rows (planes: P for a token), or its own weight's
+                const int c0 = (int)u.c0 * P + (MODE == kGated ? 0 : (int)rank * (P * u.nt / 2));
                 const uint32_t tx = 2 * (kTileBytes + kCols * u.nt / 2 * kStageK);  // both CTAs' boxes
                 for (int ks = 0; ks < p.steps; ++ks) {
                     if (!wait_cluster(&empty[s], ph ^ 1u, kWaitNs)) {
@@ -782,21 +787,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if constexpr (MODE == kGrad) {
                         const int m = ks / p.k_steps, k = (ks - m * p.k_steps) * kStageK;
                         tma_load_2d_pair(st, &maps.a[m], r0, k, bar);
-                        const int x = (int)(m * p.mat_pitch) + k;
-                        if constexpr (P == 2) {  // one plane a CTA
-                            tma_load_2d_pair(st + kTileBytes, bm, x, (int)((int64_t)rank * p.T + u.c0), bar);
-                        } else {  // three halves of planes a CTA
-#pragma unroll
-                            for (int j = 0; j < 3; ++j) {
-                                const int h = 3 * rank + j;
-                                tma_load_2d_pair(st + kTileBytes + j * (u.nt / 2) * kStageK, bm, x,
-                                                 (int)((int64_t)(h >> 1) * p.T + u.c0 + (h & 1) * (u.nt / 2)), bar);
-                            }
-                        }
+                        tma_load_2d_pair(st + kTileBytes, bm, (int)(m * p.mat_pitch) + k, c0, bar);
                     } else {
                         tma_load_2d_pair(st, &maps.a[0], ks * kStageK, r0, bar);
-                        tma_load_2d_pair(st + kTileBytes, bm, ks * kStageK,
-                                         (int)(u.c0 + (MODE == kMatmul ? rank * (u.nt / 2) : 0)), bar);
+                        tma_load_2d_pair(st + kTileBytes, bm, ks * kStageK, c0, bar);
                     }
                     if (++s == kStages) {
                         s = 0;
@@ -896,7 +890,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 break;
             }
             tc_fence_after_sync();
-            const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 256 * buf + half * cols;
+            const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 256 * buf + half * cols * P;
             if constexpr (MODE == kGated) {
                 int c = 0;
                 if (p.vec) {
@@ -954,7 +948,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 for (int c = 0; c < nv; c += 16) {
                     int v[P][16];
 #pragma unroll
-                    for (int i = 0; i < P; ++i) tmem_ld16(tl + i * un.nt + c, as_words(v[i]));
+                    for (int i = 0; i < P; ++i) tmem_ld16(tl + sum_col<MODE, P>(i, c, un.nt), as_words(v[i]));
                     tmem_wait_ld();
                     if (r0 < p.out_rows)
                         emit_channel<MODE, P, OT, 16>(co, v, c0 + c, (int)r0, nv - c, ts + c, sa, 0.0f, bias);
@@ -1061,6 +1055,12 @@ static TilePlan plan_tile(int T, int tiles_n, int steps) {
     return best;
 }
 
+// Rows of the token operand.
+template <int MODE, int P>
+static int64_t plane_rows_of(const GemmArgs& a) {
+    return MODE == kGrad ? plane_rows(P, a.T) : a.T;
+}
+
 template <int MODE, int P, typename OT>
 static cudaError_t run_tile(const GemmArgs& a, const TilePlan& plan, cudaStream_t s) {
     static bool attr_done[64];
@@ -1095,6 +1095,7 @@ static cudaError_t run_tile(const GemmArgs& a, const TilePlan& plan, cudaStream_
     }
     p.x = reinterpret_cast<const uint8_t*>(a.x);
     p.ldx = a.ldx;
+    p.x_rows = plane_rows_of<MODE, P>(a);
     p.x_unit = unit_of(a.x, a.ldx);
     if (p.x_unit < 16) p.direct = 1;
     p.mat_pitch = a.mat_pitch;
@@ -1116,7 +1117,7 @@ static cudaError_t run_tile(const GemmArgs& a, const TilePlan& plan, cudaStream_
         }
         if (a.n_mats == 1) wm[1] = wm[0];
         e = encode_2d(&xm, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, MODE == kGrad ? a.n_mats * a.mat_pitch : a.cols,
-                      (uint64_t)a.planes * a.T, a.ldx, kStageK, p.nt, CU_TENSOR_MAP_SWIZZLE_128B);
+                      p.x_rows, a.ldx, kStageK, P * p.nt, CU_TENSOR_MAP_SWIZZLE_128B);
         if (e != cudaSuccess) return e;
     }
     return launch_dense(k_dense_tile<MODE, P, OT>, (unsigned)(tiles * split), kTileThreads, smem, split, s, wm[0], wm[1], xm, p);
@@ -1196,9 +1197,9 @@ static cudaError_t run_pair(const GemmArgs& a, const PairPlan& plan, cudaStream_
     };
     auto map_x = [&](CUtensorMap* m, int box) {
         return encode_2d(m, a.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, MODE == kGrad ? a.n_mats * a.mat_pitch : a.cols,
-                         (uint64_t)a.planes * a.T, a.ldx, kStageK, box, CU_TENSOR_MAP_SWIZZLE_128B);
+                         plane_rows_of<MODE, P>(a), a.ldx, kStageK, box, CU_TENSOR_MAP_SWIZZLE_128B);
     };
-    const int half = MODE == kGrad && P == 2 ? p.nt : MODE == kGated ? p.nt : p.nt / 2;
+    const int half = MODE == kGated ? p.nt : P * p.nt / 2;
     if constexpr (MODE == kGated) {
         e = map_x(&maps.a[0], 128);
         for (int m = 0; m < 2 && e == cudaSuccess; ++m) {

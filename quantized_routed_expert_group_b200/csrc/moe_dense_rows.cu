@@ -199,10 +199,10 @@ __device__ __forceinline__ void store_planes(const GradRowsParams& p, int64_t t,
         r[i] = P == 2 ? __float_as_int(fmaf(v[i], mult, 12582912.0f)) + (0x8080 - 0x4B400000)
                       : __float2int_rn(v[i] * mult) + 0x808080;
     const int64_t row = mats * p.pitch;
-    int8_t* o = p.planes + t * row + m * p.pitch + c;
+    int8_t* o = p.planes + plane_row<P>(t) * row + m * p.pitch + c;
     store_bytes<VEC, 0>(o, r, 0x80808080u);
-    store_bytes<VEC, 1>(o + p.T * row, r, 0x80808080u);
-    if constexpr (P == 3) store_bytes<VEC, 2>(o + 2 * p.T * row, r, 0x80808080u);
+    store_bytes<VEC, 1>(o + kPlaneGroup * row, r, 0x80808080u);
+    if constexpr (P == 3) store_bytes<VEC, 2>(o + 2 * kPlaneGroup * row, r, 0x80808080u);
 }
 
 template <int VEC>

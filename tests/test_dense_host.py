@@ -108,8 +108,7 @@ def test_workspace_sizes(L):
     lib = L.lib()
     for n_mats, dtype, planes in ((1, 0, 3), (2, 0, 3), (1, 1, 2), (2, 2, 2)):
         n = lib.moe_int8_backward_workspace_bytes(n_mats, 300, 500, dtype)
-        # planes, row scales, and partial column sums
-        assert n >= planes * 300 * n_mats * 512 + 300 * 8 + (300 if n_mats == 2 else 9) * 2 * 500 * 4
+        assert n >= planes * 300 * n_mats * 512 + 300 * 8  # planes and row scales
     assert lib.moe_int8_backward_workspace_bytes(1, 0, 8, 0) > 0
     for bad in ((0, 4, 8, 0), (3, 4, 8, 0), (1, -1, 8, 0), (1, 4, 0, 0), (1, 4, 8, 5), (2, 4, 65536, 0)):
         assert lib.moe_int8_backward_workspace_bytes(*bad) == 0
