@@ -365,7 +365,14 @@ int moe_get_device_error(void *workspace, void *stream, int32_t *code);
  * T up to 2^28, contractions (cols; in a backward pass the number of matrices
  * times rows) up to 131071, so that every int32 sum is exact, else
  * MOE_EUNSUPPORTED.  The current device must be the one that holds the data.
- * Results do not depend on timing: equal calls give equal bits on one device.
+ * Results must not overlap inputs, the workspace or one another.  Calls may run
+ * at the same time on several streams, each with its own results and workspace,
+ * and may be captured into graphs.  Results do not depend on timing: equal calls
+ * give equal bits on one device.  A result is fp32 arithmetic on exact integer
+ * sums, rounded once to its type; the activation's sigmoid uses a reciprocal
+ * good to two units in the last place.  A token whose scale is NaN (see
+ * moe_quantize_act_token) gives NaN in its row of every product.
+ * Codes take all values from -128 to 127.
  * ------------------------------------------------------------------------- */
 enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 }; /* element types */
 /* Activations of the gated block, act(g) = g sigmoid(z): z = g (SiLU), or
@@ -412,9 +419,10 @@ size_t moe_int8_backward_workspace_bytes(int n_mats, int T, int rows, int dtype)
  *   dx[t][k] = sum_n dy[t][n] s[n] w[n][k]  (type dtype)
  *   ds[n] = sum_t dy[t][n] xd[t] acc[t][n],  dbias[n] = sum_t dy[t][n]  (fp32)
  * ds and dbias may be NULL; acc and xd are needed for ds only (NULL
- * otherwise).  The rows dy s are written as fixed-point numbers of 15 bits and
- * a sign relative to the row's largest (23 bits for fp32) and multiplied
- * exactly; a row with an infinity or a NaN gives NaN in its row of dx.
+ * otherwise).  The rows dy s are written as fixed-point numbers relative to the
+ * row's largest, 16 bits for 16-bit types and 24 for fp32, and multiplied
+ * exactly: an element is off by at most 2^-16 (2^-24) of the largest.  A row
+ * with an infinity or a NaN gives NaN in its row of dx.
  * workspace: >= moe_int8_backward_workspace_bytes(1, T, rows, dtype) bytes,
  * 256-byte aligned; nothing in it is kept between calls. */
 int moe_int8_matmul_backward(const void *dy, int dtype, int64_t lddy, const int32_t *acc, const float *xd, int T,
