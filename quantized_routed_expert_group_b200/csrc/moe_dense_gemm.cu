@@ -36,7 +36,9 @@ __device__ int32_t g_dense_error;
 constexpr uint64_t kWaitNs = 100000000ull;  // one pipeline wait
 constexpr uint64_t kWaitAllNs = 4 * kWaitNs;  // the epilogue's wait for the whole tile
 constexpr int kMaxStages = 8;
-constexpr int kTileThreads = 192;  // producer warp, MMA warp, four epilogue warps
+constexpr int kTileThreads = 192;    // producer warp, MMA warp, four epilogue warps
+constexpr int kDirectThreads = 320;  // with operands off the 16-byte grid: eight warps that load, four of them the epilogue
+constexpr int kLoaders = kDirectThreads - 64;
 constexpr int kCtlBytes = 2048;    // barriers, the TMEM address, 128 token scales
 
 struct TileParams {
@@ -108,7 +110,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* row, int64_t
 }
 
 // A tile of n rows of 128 bytes at (row0, col0) of [rows][cols] into the
-// 128-byte-swizzle layout, by 128 threads (16 rows a pass); bytes outside read
+// 128-byte-swizzle layout, by kLoaders threads (32 rows a pass); bytes outside read
 // as zero.  Rows on a 16-, 8- or 4-byte grid are copied asynchronously (the
 // caller commits and waits); others are put together from aligned words, four
 // passes of loads under way at a time.
@@ -118,7 +120,7 @@ __device__ __forceinline__ void load_tile_direct(uint8_t* tile, const uint8_t* b
     const int64_t col = col0 + 16 * c;
     const int in_row = (int)min((int64_t)16, max((int64_t)0, cols - col));  // bytes of the chunk inside the row
     if (unit >= 4) {
-        for (int r = tid >> 3; r < n; r += 16) {
+        for (int r = tid >> 3; r < n; r += kLoaders / 8) {
             const bool ok = row0 + r < rows;
             const uint8_t* row = base + (ok ? row0 + r : 0) * ld;
             const uint32_t dst = smem_addr(tile + sw128_chunk(r, c));
@@ -132,17 +134,17 @@ __device__ __forceinline__ void load_tile_direct(uint8_t* tile, const uint8_t* b
         }
         return;
     }
-    for (int r0 = tid >> 3; r0 < n; r0 += 64) {
+    for (int r0 = tid >> 3; r0 < n; r0 += kLoaders / 2) {
         Words w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int r = r0 + 16 * k;
+            const int r = r0 + kLoaders / 8 * k;
             const bool ok = r < n && row0 + r < rows;
             w[k] = load_words(base + (ok ? row0 + r : 0) * ld + col, ok ? in_row : 0);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int r = r0 + 16 * k;
+            const int r = r0 + kLoaders / 8 * k;
             if (r < n) *reinterpret_cast<uint4*>(tile + sw128_chunk(r, c)) = join_words(w[k]);
         }
     }
@@ -256,7 +258,7 @@ __device__ __forceinline__ void emit_channel(const ChannelOut& o, const int (&v)
 // (exact, so the split changes no bit).  Every wait is bounded by the global
 // timer and records kErrTimeout.
 template <int MODE, int P, typename OT>
-__global__ void __launch_bounds__(kTileThreads)
+__global__ void __launch_bounds__(kDirectThreads)
     k_dense_tile(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUtensorMap wmap1,
                  const __grid_constant__ CUtensorMap xmap, const TileParams p) {
     constexpr int kV = MODE == kGated ? 2 : P;         // sums of a result element
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kTileThreads)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], p.direct ? 128 : 1);
+            mbar_init(&full[s], p.direct ? kLoaders : 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(accf, 1);
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kTileThreads)
     }
     pdl_wait();
     pdl_launch_dependents();
-    for (int i = threadIdx.x; i < p.nt; i += kTileThreads)
+    for (int i = threadIdx.x; i < p.nt; i += blockDim.x)
         tok[i] = i >= nv ? RowScale{0.0f, 0.0f} : MODE == kGrad ? p.gscale[t0 + i] : RowScale{p.xd[t0 + i], 1.0f};
     tc_fence_before_sync();
     __syncthreads();
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(kTileThreads)
     float s0 = 0.0f, s1 = 0.0f, bias = 0.0f;
     int32_t* part = reinterpret_cast<int32_t*>(sm);  // split: [column][128] sums of this CTA
     const ChannelOut co{p.out, p.ldo, p.acc, (int64_t)p.T * p.rows, p.rows, p.act};
-    if (warp >= 2) {
+    if (warp >= 2 && warp < 6) {
         if constexpr (MODE != kGrad) {
             if (n < p.out_rows) {
                 s0 = p.s[0][n];
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kTileThreads)
                     if (MODE == kMatmul && p.bias) bq[k] = p.bias[nq + k];
                 }
         }
-        for (int c = (int)rank + (int)split * warp; c < nv; c += (int)split * (kTileThreads / 32)) {
+        for (int c = (int)rank + (int)split * warp; c < nv; c += (int)split * (int)(blockDim.x / 32)) {
             int4 w[8][kV];
 #pragma unroll
             for (uint32_t q = 0; q < 8; ++q)
@@ -1120,7 +1122,8 @@ static cudaError_t run_tile(const GemmArgs& a, const TilePlan& plan, cudaStream_
                       p.x_rows, a.ldx, kStageK, P * p.nt, CU_TENSOR_MAP_SWIZZLE_128B);
         if (e != cudaSuccess) return e;
     }
-    return launch_dense(k_dense_tile<MODE, P, OT>, (unsigned)(tiles * split), kTileThreads, smem, split, s, wm[0], wm[1], xm, p);
+    return launch_dense(k_dense_tile<MODE, P, OT>, (unsigned)(tiles * split),
+                        p.direct ? kDirectThreads : kTileThreads, smem, split, s, wm[0], wm[1], xm, p);
 }
 
 // Columns of a pair's tile (channels of the gated block, tokens elsewhere).
