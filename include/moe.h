@@ -359,8 +359,10 @@ int moe_get_device_error(void *workspace, void *stream, int32_t *code);
  * For all of them: matrices are row-major with a row stride in ELEMENTS (ld*,
  * at least the row's length; what lies between the rows is neither read nor
  * written); any number of rows and columns is supported within the limits
- * below, and any alignment that fits the element type (rows whose address or
- * stride is no multiple of 16 bytes take plain loads instead of TMA).
+ * below, and any alignment that fits the element type.  Rows of codes whose
+ * address or stride is no multiple of 16 bytes are copied to such ones in the
+ * workspace where that pays and the workspace has room, and otherwise loaded as
+ * they lie, which is slower.
  * T = 0 returns MOE_OK (gradients that sum over tokens are then set to zero).
  * T up to 2^28, contractions (cols; in a backward pass the number of matrices
  * times rows) up to 131071, so that every int32 sum is exact, else
@@ -387,15 +389,21 @@ enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1 };
 int moe_quantize_act_token(const void *x, int dtype, int64_t n_rows, int cols, int64_t ldx, int8_t *q, int64_t ldq,
                            float *d, void *stream);
 
+/* Bytes of device workspace with which moe_int8_matmul (n_mats 1) and
+ * moe_gated_ffn (n_mats 2) copy rows off the 16-byte grid (cols no multiple of
+ * 16); 0 where they would not use one, or when an argument is out of range. */
+size_t moe_int8_forward_workspace_bytes(int n_mats, int T, int rows, int cols);
+
 /* Integer product with scales for each token and channel:
  *   acc[t][n] = sum_k xq[t][k] * w[n][k]              (int32, exact)
  *   out[t][n] = acc[t][n] * (xd[t] * s[n]) + bias[n]  (fp32, rounded once to dtype)
  * for xq [T][cols], w [rows][cols], s [rows], bias [rows] or NULL.  acc
  * [T][rows] (dense) receives the integer sums for moe_int8_matmul_backward;
- * NULL leaves them out. */
+ * NULL leaves them out.  workspace (256-byte aligned) may be NULL or too small:
+ * see moe_int8_forward_workspace_bytes; nothing in it is kept between calls. */
 int moe_int8_matmul(const int8_t *xq, int64_t ldx, const float *xd, int T, const uint8_t *w, int64_t ldw,
                     const float *s, int rows, int cols, const float *bias, void *out, int dtype, int64_t ldo,
-                    int32_t *acc, void *stream);
+                    int32_t *acc, void *workspace, size_t ws_bytes, void *stream);
 
 /* Gated feed-forward block, both projections, the activation and the product
  * in one kernel:
@@ -403,15 +411,17 @@ int moe_int8_matmul(const int8_t *xq, int64_t ldx, const float *xd, int T, const
  *   out[t][i] = act(g) * u                            (fp32, rounded once to dtype)
  * with the sums of moe_int8_matmul over w_gate and w_up [rows][cols].  acc
  * [2][T][rows] (gate, then up) receives the integer sums for
- * moe_gated_ffn_backward; NULL leaves them out. */
+ * moe_gated_ffn_backward; NULL leaves them out.  workspace as for
+ * moe_int8_matmul. */
 int moe_gated_ffn(const int8_t *xq, int64_t ldx, const float *xd, int T, const uint8_t *w_gate, int64_t ldg,
                   const float *s_gate, const uint8_t *w_up, int64_t ldu, const float *s_up, int rows, int cols,
-                  int act, void *out, int dtype, int64_t ldo, int32_t *acc, void *stream);
+                  int act, void *out, int dtype, int64_t ldo, int32_t *acc, void *workspace, size_t ws_bytes,
+                  void *stream);
 
 /* Bytes of device workspace of the backward passes, with n_mats = 1 for
  * moe_int8_matmul_backward and 2 for moe_gated_ffn_backward (0 when an
  * argument is out of range). */
-size_t moe_int8_backward_workspace_bytes(int n_mats, int T, int rows, int dtype);
+size_t moe_int8_backward_workspace_bytes(int n_mats, int T, int rows, int cols, int dtype);
 
 /* Backward pass of moe_int8_matmul for dy [T][rows] (type dtype).  The codes
  * are constants; gradients reach the dequantised activations x = xd * xq, the
@@ -423,7 +433,7 @@ size_t moe_int8_backward_workspace_bytes(int n_mats, int T, int rows, int dtype)
  * row's largest, 16 bits for 16-bit types and 24 for fp32, and multiplied
  * exactly: an element is off by at most 2^-16 (2^-24) of the largest.  A row
  * with an infinity or a NaN gives NaN in its row of dx.
- * workspace: >= moe_int8_backward_workspace_bytes(1, T, rows, dtype) bytes,
+ * workspace: >= moe_int8_backward_workspace_bytes(1, T, rows, cols, dtype) bytes,
  * 256-byte aligned; nothing in it is kept between calls. */
 int moe_int8_matmul_backward(const void *dy, int dtype, int64_t lddy, const int32_t *acc, const float *xd, int T,
                              const uint8_t *w, int64_t ldw, const float *s, int rows, int cols, void *dx,

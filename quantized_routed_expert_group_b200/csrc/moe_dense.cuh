@@ -249,10 +249,10 @@ __device__ __forceinline__ uint4 ld_once_v4(const void* p) {
 }
 
 template <typename... P, typename... A>
-cudaError_t launch_dense(void (*kernel)(P...), unsigned grid, int threads, size_t smem, int cluster, cudaStream_t s,
+cudaError_t launch_dense(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s,
                          A&&... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -371,6 +371,21 @@ cudaError_t launch_gated_quantised(const GemmArgs& a, const void* x, int x_type,
 cudaError_t launch_matmul_quantised(const GemmArgs& a, const float* x, cudaStream_t s);
 cudaError_t launch_grad_matmul(const GemmArgs& a, cudaStream_t s);
 cudaError_t read_device_error(cudaStream_t s, int32_t* code);
+
+// Whether TMA can take every operand: addresses and row strides on 16 bytes.
+inline bool tma_operands(const GemmArgs& a) {
+    bool ok = unit_of(a.x, a.ldx) == 16;
+    for (int m = 0; m < a.n_mats; ++m) ok = ok && unit_of(a.w[m], a.ldw[m]) == 16;
+    return ok;
+}
+
+// Copies the operands that are off the 16-byte grid to rows of pad_pitch(cols)
+// bytes in `room` (pad_bytes), and points `a` at them.  A pass over odd rows
+// costs their bytes twice and a launch; the products' own loads of them cost
+// about four times what TMA does (2000 x 2049 x 3001: 106 us as they lie).
+inline int64_t pad_pitch(int cols) { return ((int64_t)cols + 15) / 16 * 16; }
+size_t pad_bytes(int n_mats, int T, int rows, int cols);
+cudaError_t pad_operands(GemmArgs& a, bool tokens, void* room, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // Row kernels (moe_dense_rows.cu)

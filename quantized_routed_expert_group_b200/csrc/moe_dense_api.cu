@@ -43,12 +43,20 @@ static int check_matrix(const void* p, int dtype, int64_t ld, int cols) {
     return p && aligned(p, elem_size(dtype)) && ld >= cols ? MOE_OK : MOE_EINVAL;
 }
 
+// Copies of odd rows pay from about a megabyte on (333 x 1001 x 777: 12.0 -> 8.5 us;
+// 300 x 1000 x 500, 0.8 MB: 8.1 -> 8.7 us), and not for the few tokens that stream
+// the weights.
+static size_t forward_room(int n_mats, int T, int rows, int cols) {
+    const size_t n = pad_bytes(n_mats, T, rows, cols);
+    return cols % 16 && T > kFewTokens && n >= 1u << 20 ? align256(n) : 0;
+}
+
 struct BackwardLayout {
-    size_t planes, scale, partials, done, total;
+    size_t planes, scale, partials, done, room, total;
     int64_t pitch;
 };
 
-static BackwardLayout backward_layout(int n_mats, int T, int rows, int dtype) {
+static BackwardLayout backward_layout(int n_mats, int T, int rows, int cols, int dtype) {
     BackwardLayout L;
     L.pitch = ((int64_t)rows + 127) / 128 * 128;
     L.planes = 0;
@@ -56,11 +64,18 @@ static BackwardLayout backward_layout(int n_mats, int T, int rows, int dtype) {
     L.partials = L.scale + align256((size_t)T * sizeof(RowScale));
     const size_t parts = n_mats == 2 ? grad_rows_grid(T) : T / 32 < kMaxDotChunks ? T / 32 : kMaxDotChunks;
     L.done = L.partials + align256(parts * 2 * rows * sizeof(float));
-    L.total = L.done + (n_mats == 2 ? 0 : align256(col_dots_tiles(rows) * sizeof(int)));
+    L.room = L.done + (n_mats == 2 ? 0 : align256(col_dots_tiles(rows) * sizeof(int)));
+    // the weights alone; at every size measured (300 x 1000 x 500: 14.1 -> 12.8 us)
+    L.total = L.room + (cols % 16 ? align256(pad_bytes(n_mats, 0, rows, cols)) : 0);
     return L;
 }
 
-static int forward(GemmArgs& a, bool gated, cudaStream_t s) {
+static int forward(GemmArgs& a, bool gated, void* workspace, size_t ws_bytes, cudaStream_t s) {
+    const size_t room = forward_room(a.n_mats, a.T, a.rows, a.cols);
+    if (room && workspace && ws_bytes >= room && !tma_operands(a)) {
+        const int st = status_of(pad_operands(a, true, workspace, s));
+        if (st) return st;
+    }
     return status_of(gated ? launch_gated(a, s) : launch_matmul(a, s));
 }
 
@@ -74,7 +89,7 @@ static int backward(int n_mats, const void* dy, int dtype, int64_t lddy, const i
         return MOE_OK;
     }
     if (!workspace || !aligned(workspace, 256)) return MOE_EINVAL;
-    const BackwardLayout L = backward_layout(n_mats, T, rows, dtype);
+    const BackwardLayout L = backward_layout(n_mats, T, rows, cols, dtype);
     if (ws_bytes < L.total) return MOE_EWORKSPACE;
     char* ws = static_cast<char*>(workspace);
     GradRowsArgs r{};
@@ -112,7 +127,8 @@ static int backward(int n_mats, const void* dy, int dtype, int64_t lddy, const i
     g.out = dx;
     g.ldo = lddx;
     g.dtype = dtype;
-    st = status_of(launch_grad_matmul(g, s));
+    if (L.total > L.room) st = status_of(pad_operands(g, false, ws + L.room, s));
+    if (!st) st = status_of(launch_grad_matmul(g, s));
     if (!st && (sum0 || sum1))
         st = status_of(n_mats == 2 ? launch_col_sums(r.partials, n_part, rows, sum0, sum1, s)
                                    : launch_col_dots(r, sum0, sum1, s));
@@ -120,7 +136,7 @@ static int backward(int n_mats, const void* dy, int dtype, int64_t lddy, const i
 }
 
 struct FfnLayout {
-    size_t xq, xd, h, hq, hd, total;
+    size_t xq, xd, h, hq, hd, room, total;
     int64_t ldx, ldh;
 };
 
@@ -139,6 +155,9 @@ static FfnLayout ffn_layout(int T, int hidden, int inter) {
     L.h = take((size_t)T * L.ldh * 4);
     L.hq = take((size_t)T * L.ldh);
     L.hd = take((size_t)T * 4);
+    // one room for both products' odd rows
+    const size_t up = forward_room(2, T, inter, hidden), down = forward_room(1, T, hidden, inter);
+    L.room = take(up > down ? up : down);
     L.total = off;
     return L;
 }
@@ -159,13 +178,13 @@ MOE_API int moe_quantize_act_token(const void* x, int dtype, int64_t n_rows, int
 
 MOE_API int moe_int8_matmul(const int8_t* xq, int64_t ldx, const float* xd, int T, const uint8_t* w, int64_t ldw,
                             const float* s, int rows, int cols, const float* bias, void* out, int dtype, int64_t ldo,
-                            int32_t* acc, void* stream) {
+                            int32_t* acc, void* workspace, size_t ws_bytes, void* stream) {
     int st = check_sizes(T, rows, cols, dtype);
     if (st) return st;
     if (cols > kMaxContraction) return MOE_EUNSUPPORTED;
     st = check_weight(w, ldw, s, cols);
     if (st) return st;
-    if (!aligned(bias, 4) || !aligned(acc, 4)) return MOE_EINVAL;
+    if (!aligned(bias, 4) || !aligned(acc, 4) || !aligned(workspace, 256)) return MOE_EINVAL;
     if (T == 0) return MOE_OK;
     if (!xq || ldx < cols || !xd || !aligned(xd, 4) || check_matrix(out, dtype, ldo, rows)) return MOE_EINVAL;
     const NvtxRange range("moe/int8_matmul");
@@ -185,12 +204,13 @@ MOE_API int moe_int8_matmul(const int8_t* xq, int64_t ldx, const float* xd, int 
     a.ldo = ldo;
     a.dtype = dtype;
     a.acc = acc;
-    return forward(a, false, (cudaStream_t)stream);
+    return forward(a, false, workspace, ws_bytes, (cudaStream_t)stream);
 }
 
 MOE_API int moe_gated_ffn(const int8_t* xq, int64_t ldx, const float* xd, int T, const uint8_t* w_gate, int64_t ldg,
                           const float* s_gate, const uint8_t* w_up, int64_t ldu, const float* s_up, int rows,
-                          int cols, int act, void* out, int dtype, int64_t ldo, int32_t* acc, void* stream) {
+                          int cols, int act, void* out, int dtype, int64_t ldo, int32_t* acc, void* workspace,
+                          size_t ws_bytes, void* stream) {
     int st = check_sizes(T, rows, cols, dtype);
     if (st) return st;
     if (!known_act(act)) return MOE_EINVAL;
@@ -198,7 +218,7 @@ MOE_API int moe_gated_ffn(const int8_t* xq, int64_t ldx, const float* xd, int T,
     st = check_weight(w_gate, ldg, s_gate, cols);
     if (!st) st = check_weight(w_up, ldu, s_up, cols);
     if (st) return st;
-    if (!aligned(acc, 4)) return MOE_EINVAL;
+    if (!aligned(acc, 4) || !aligned(workspace, 256)) return MOE_EINVAL;
     if (T == 0) return MOE_OK;
     if (!xq || ldx < cols || !xd || !aligned(xd, 4) || check_matrix(out, dtype, ldo, rows)) return MOE_EINVAL;
     const NvtxRange range("moe/gated_ffn");
@@ -221,14 +241,20 @@ MOE_API int moe_gated_ffn(const int8_t* xq, int64_t ldx, const float* xd, int T,
     a.ldo = ldo;
     a.dtype = dtype;
     a.acc = acc;
-    return forward(a, true, (cudaStream_t)stream);
+    return forward(a, true, workspace, ws_bytes, (cudaStream_t)stream);
 }
 
-MOE_API size_t moe_int8_backward_workspace_bytes(int n_mats, int T, int rows, int dtype) {
-    if (n_mats < 1 || n_mats > kMaxMats || T < 0 || T > kMaxTokens || rows <= 0 ||
+MOE_API size_t moe_int8_forward_workspace_bytes(int n_mats, int T, int rows, int cols) {
+    if (n_mats < 1 || n_mats > kMaxMats || T < 0 || T > kMaxTokens || rows <= 0 || cols <= 0 || cols > kMaxContraction)
+        return 0;
+    return forward_room(n_mats, T, rows, cols);
+}
+
+MOE_API size_t moe_int8_backward_workspace_bytes(int n_mats, int T, int rows, int cols, int dtype) {
+    if (n_mats < 1 || n_mats > kMaxMats || T < 0 || T > kMaxTokens || rows <= 0 || cols <= 0 ||
         (int64_t)n_mats * rows > kMaxContraction || !known_type(dtype))
         return 0;
-    const size_t n = backward_layout(n_mats, T, rows, dtype).total;
+    const size_t n = backward_layout(n_mats, T, rows, cols, dtype).total;
     return n ? n : 256;
 }
 
@@ -333,11 +359,11 @@ MOE_API int moe_dense_ffn(const void* x, int dtype, int64_t ldx, int T, int hidd
     st = moe_quantize_act_token(x, dtype, T, hidden, ldx, xq, L.ldx, xd, stream);
     if (!st)
         st = moe_gated_ffn(xq, L.ldx, xd, T, experts->w_gate, hidden, experts->s_gate, experts->w_up, hidden,
-                           experts->s_up, inter, hidden, act, h, MOE_F32, L.ldh, nullptr, stream);
+                           experts->s_up, inter, hidden, act, h, MOE_F32, L.ldh, nullptr, ws + L.room, L.total - L.room, stream);
     if (!st) st = moe_quantize_act_token(h, MOE_F32, T, inter, L.ldh, hq, L.ldh, hd, stream);
     if (!st)
         st = moe_int8_matmul(hq, L.ldh, hd, T, experts->w_down, inter, experts->s_down, hidden, inter, nullptr, out,
-                             dtype, ldo, nullptr, stream);
+                             dtype, ldo, nullptr, ws + L.room, L.total - L.room, stream);
     return st;
 }
 

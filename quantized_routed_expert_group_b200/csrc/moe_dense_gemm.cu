@@ -650,36 +650,6 @@ __device__ __forceinline__ PairUnit pair_unit(const PairParams& p, int64_t u) {
     return PairUnit{tile % p.tiles_r * kPairRows, tile / p.tiles_r * p.nt + sub * nt, nt, part};
 }
 
-// Sixteen results of one token, channels n .. n + 15.
-template <typename OT>
-__device__ __forceinline__ void store16(const PairParams& p, int64_t t, int n, const float (&v)[16]) {
-    OT* o = static_cast<OT*>(p.out) + t * p.ldo + n;
-    alignas(16) OT e[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) e[i] = from_f32<OT>(v[i]);
-    if (p.vec && n + 16 <= p.out_rows) {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(e) / 16; ++i)
-            reinterpret_cast<uint4*>(o)[i] = reinterpret_cast<const uint4*>(e)[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (n + i < p.out_rows) o[i] = e[i];
-    }
-}
-
-__device__ __forceinline__ void store_acc16(const PairParams& p, int32_t* row, int n, const uint32_t (&v)[16]) {
-    if (p.vec && n + 16 <= p.out_rows) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4*>(row + n)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (n + i < p.out_rows) row[n + i] = (int)v[i];
-    }
-}
-
 // 32 consecutive 32-bit columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile(
@@ -693,25 +663,39 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
         : "memory");
 }
 
-// 32 values of each of a warp's 32 rows (a lane holds its row's columns n ..
-// n + 31) to rows t0 .. of [T][N] at n, through the warp's staging buffer: a row
-// is written by 32 * sizeof(V) / 16 neighbouring lanes.  N and ld are multiples of 16 bytes.
-template <typename V, typename W>
-__device__ __forceinline__ void store_rows32(V* out, int64_t ld, int64_t T, int N, int64_t t0, int n,
-                                             const W (&v)[32], uint8_t* stage, int lane) {
+__device__ __forceinline__ void tmem_ld_columns(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld32(taddr, v); }
+__device__ __forceinline__ void tmem_ld_columns(uint32_t taddr, uint32_t (&v)[16]) { tmem_ld16(taddr, v); }
+
+// C values of each of a warp's 32 rows (a lane holds its row's columns n ..
+// n + C - 1) to rows t0 .. of [T][N] at n, through the warp's staging buffer: a row
+// is written by C * sizeof(V) / 16 neighbouring lanes, 16 bytes each, where out,
+// N and ld are multiples of that (vec), and by C lanes an element each elsewhere.
+// (Each lane storing its own odd row took 97 us in place of 38 at 2000 x 2049 x
+// 3001, gated.)
+template <typename V, typename W, int C>
+__device__ __forceinline__ void store_rows(V* out, int64_t ld, int64_t T, int N, int64_t t0, int n, const W (&v)[C],
+                                           int vec, uint8_t* stage, int lane) {
     static_assert(sizeof(V) == sizeof(W), "the same elements");
-    constexpr int kPieces = 32 * (int)sizeof(V) / 16, kPitch = 16 * kPieces + 16, kEach = 16 / (int)sizeof(V);
+    constexpr int kPieces = C * (int)sizeof(V) / 16, kPitch = 16 * kPieces + 16, kEach = 16 / (int)sizeof(V);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
         *reinterpret_cast<uint4*>(stage + lane * kPitch + 16 * i) = reinterpret_cast<const uint4*>(v)[i];
     __syncwarp();
-    const int piece = lane % kPieces;
-    const bool in = n + (piece + 1) * kEach <= N;
+    if (vec) {
+        const int piece = lane % kPieces;
+        const bool in = n + (piece + 1) * kEach <= N;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-        const int row = i * (32 / kPieces) + lane / kPieces;
-        const uint4 w = *reinterpret_cast<const uint4*>(stage + row * kPitch + 16 * piece);
-        if (in && t0 + row < T) *reinterpret_cast<uint4*>(out + (t0 + row) * ld + n + piece * kEach) = w;
+        for (int i = 0; i < kPieces; ++i) {
+            const int row = i * (32 / kPieces) + lane / kPieces;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + row * kPitch + 16 * piece);
+            if (in && t0 + row < T) *reinterpret_cast<uint4*>(out + (t0 + row) * ld + n + piece * kEach) = w;
+        }
+    } else if (n + lane % C < N) {
+        const int nr = (int)(T - t0 < 32 ? T - t0 : 32);
+        V* o = out + t0 * ld + n + lane % C;
+#pragma unroll 8
+        for (int row = lane / C; row < nr; row += 32 / C)
+            o[row * ld] = *reinterpret_cast<const V*>(stage + row * kPitch + lane % C * (int)sizeof(V));
     }
     __syncwarp();
 }
@@ -894,56 +878,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tc_fence_after_sync();
             const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 256 * buf + half * cols * P;
             if constexpr (MODE == kGated) {
-                int c = 0;
-                if (p.vec) {
-                    // 32 channels at a time, turned in shared memory so that the
-                    // stores run along the tokens' rows
-                    uint8_t* stage = sm + kStages * kStage + (warp - 2) * kStageWarp;
-                    const int64_t t0 = r0 - lane;
-                    for (; c + 32 <= cols; c += 32) {
-                        uint32_t g[32], u[32];
-                        tmem_ld32(tl + c, g);
-                        tmem_ld32(tl + un.nt + c, u);
-                        tmem_wait_ld();
-                        if (p.acc) {
-                            store_rows32(p.acc, p.rows, p.T, p.rows, t0, (int)c0 + c, g, stage, lane);
-                            store_rows32(p.acc + p.T * (int64_t)p.rows, p.rows, p.T, p.rows, t0, (int)c0 + c, u,
-                                         stage, lane);
-                        }
-                        alignas(16) OT h[32];
-                        with_act(p.act, [&](auto act) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const RowScale sc = ts[c + j];
-                                h[j] = from_f32<OT>(
-                                    act_value<decltype(act)::value>((float)(int)g[j] * (sa * sc.a)) *
-                                    ((float)(int)u[j] * (sa * sc.b)));
-                            }
-                        });
-                        store_rows32(static_cast<OT*>(p.out), p.ldo, p.T, p.rows, t0, (int)c0 + c, h, stage, lane);
-                    }
-                }
-                for (; c < cols; c += 16) {
-                    uint32_t g[16], u[16];
-                    tmem_ld16(tl + c, g);
-                    tmem_ld16(tl + un.nt + c, u);
+                // 32 channels at a time (16 where a unit has no more), turned in shared
+                // memory so that the stores run along the tokens' rows
+                uint8_t* stage = sm + kStages * kStage + (warp - 2) * kStageWarp;
+                const int64_t t0 = r0 - lane;
+                auto columns = [&](int c, auto width) {
+                    constexpr int C = decltype(width)::value;
+                    alignas(16) uint32_t g[C], u[C];
+                    tmem_ld_columns(tl + c, g);
+                    tmem_ld_columns(tl + un.nt + c, u);
                     tmem_wait_ld();
-                    if (r0 < p.T) {
-                        float h[16];
-                        with_act(p.act, [&](auto act) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const RowScale sc = ts[c + j];
-                                h[j] = act_value<decltype(act)::value>((float)(int)g[j] * (sa * sc.a)) *
-                                       ((float)(int)u[j] * (sa * sc.b));
-                            }
-                        });
-                        store16<OT>(p, r0, (int)c0 + c, h);
-                        if (p.acc) {
-                            store_acc16(p, p.acc + r0 * p.rows, (int)c0 + c, g);
-                            store_acc16(p, p.acc + (p.T + r0) * p.rows, (int)c0 + c, u);
-                        }
+                    const int n = (int)c0 + c;
+                    if (p.acc) {
+                        store_rows(p.acc, p.rows, p.T, p.rows, t0, n, g, p.vec, stage, lane);
+                        store_rows(p.acc + p.T * (int64_t)p.rows, p.rows, p.T, p.rows, t0, n, u, p.vec, stage, lane);
                     }
+                    alignas(16) OT h[C];
+                    with_act(p.act, [&](auto act) {
+#pragma unroll
+                        for (int j = 0; j < C; ++j) {
+                            const RowScale sc = ts[c + j];
+                            h[j] = from_f32<OT>(act_value<decltype(act)::value>((float)(int)g[j] * (sa * sc.a)) *
+                                                ((float)(int)u[j] * (sa * sc.b)));
+                        }
+                    });
+                    store_rows(static_cast<OT*>(p.out), p.ldo, p.T, p.rows, t0, n, h, p.vec, stage, lane);
+                };
+                if (cols % 32 == 0) {
+                    for (int c = 0; c < cols; c += 32) columns(c, std::integral_constant<int, 32>{});
+                } else {
+                    for (int c = 0; c < cols; c += 16) columns(c, std::integral_constant<int, 16>{});
                 }
             } else {
                 const int nv = (int)min((int64_t)cols, p.T - c0);
@@ -1224,13 +1188,6 @@ static cudaError_t run_pair(const GemmArgs& a, const PairPlan& plan, cudaStream_
     const int64_t pairs = device_info().sm_count / 2;
     const unsigned grid = 2 * (unsigned)(p.units < pairs ? p.units : pairs);
     return launch_dense(k_dense_pair<MODE, P, OT>, grid, kPairThreads, kPairSmem<MODE>, 1, s, maps, p);
-}
-
-// Whether TMA can take every operand: addresses and row strides on 16 bytes.
-static bool tma_operands(const GemmArgs& a) {
-    bool ok = unit_of(a.x, a.ldx) == 16;
-    for (int m = 0; m < a.n_mats; ++m) ok = ok && unit_of(a.w[m], a.ldw[m]) == 16;
-    return ok;
 }
 
 // Single CTAs or pairs, by their estimates (within 20 % of the better one over 17

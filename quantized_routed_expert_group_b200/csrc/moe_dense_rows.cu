@@ -638,5 +638,85 @@ cudaError_t launch_col_dots(const GradRowsArgs& a, float* ds, float* dbias, cuda
                                  : col_dots<MOE_F16>(a, ds, dbias, s);
 }
 
+// ---------------------------------------------------------------------------
+// Rows of codes off the 16-byte grid to rows on it (bytes past a row's end are
+// left: the products read rows by their length).  Up to three matrices a launch,
+// one for each blockIdx.y, in chunks of 16 bytes, EACH of them under way a thread
+// (1 while the threads find room on the device at once).  Bound by latency at a
+// few megabytes, by memory beyond.
+// ---------------------------------------------------------------------------
+struct PadParams {
+    const uint8_t* src[3];
+    int64_t ld[3];
+    int64_t chunks[3];  // of the matrix
+    uint8_t* dst[3];
+    int unit[3];
+    int n, cols;
+    uint32_t row_chunks;
+};
+
+template <int EACH>
+__global__ void __launch_bounds__(256) k_pad_rows(const PadParams p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    // (chosen by comparisons: an index would put the parameters on the stack)
+    const int m = blockIdx.y;
+    const uint8_t* src = m == 0 ? p.src[0] : m == 1 ? p.src[1] : p.src[2];
+    uint8_t* dst = m == 0 ? p.dst[0] : m == 1 ? p.dst[1] : p.dst[2];
+    const int64_t ld = m == 0 ? p.ld[0] : m == 1 ? p.ld[1] : p.ld[2];
+    const int64_t n = m == 0 ? p.chunks[0] : m == 1 ? p.chunks[1] : p.chunks[2];
+    const int unit = m == 0 ? p.unit[0] : m == 1 ? p.unit[1] : p.unit[2];
+    for (int64_t i0 = (int64_t)blockIdx.x * (256 * EACH) + threadIdx.x; i0 < n; i0 += (int64_t)gridDim.x * (256 * EACH)) {
+        uint4 v[EACH];
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            const int64_t i = i0 + 256 * e;
+            const uint32_t r = (uint32_t)i / p.row_chunks, c = (uint32_t)i - r * p.row_chunks;
+            if (i < n) v[e] = load16(src + r * ld, 16 * (int64_t)c, p.cols, unit);
+        }
+#pragma unroll
+        for (int e = 0; e < EACH; ++e)
+            if (i0 + 256 * e < n) *reinterpret_cast<uint4*>(dst + 16 * (i0 + 256 * e)) = v[e];
+    }
+}
+
+size_t pad_bytes(int n_mats, int T, int rows, int cols) {
+    return ((size_t)n_mats * rows + T) * (size_t)pad_pitch(cols);
+}
+
+cudaError_t pad_operands(GemmArgs& a, bool tokens, void* room, cudaStream_t s) {
+    PadParams p{};
+    p.cols = a.cols;
+    const int64_t pitch = pad_pitch(a.cols);
+    p.row_chunks = (uint32_t)(pitch / 16);
+    uint8_t* to = static_cast<uint8_t*>(room);
+    int64_t most = 0;
+    // the copy of one matrix: its address, with the pitch as its stride from then on
+    auto copy = [&](const void* src, int64_t& ld, int rows) {
+        const int i = p.n++;
+        p.src[i] = static_cast<const uint8_t*>(src);
+        p.ld[i] = ld;
+        p.chunks[i] = (int64_t)rows * p.row_chunks;
+        p.dst[i] = to;
+        p.unit[i] = unit_of(src, ld);
+        to += rows * pitch;
+        most = p.chunks[i] > most ? p.chunks[i] : most;
+        ld = pitch;
+        return p.dst[i];
+    };
+    // (chunks are counted in 32 bits: larger matrices are read as they lie)
+    const bool w_fits = (int64_t)a.rows * p.row_chunks <= UINT32_MAX;
+    const bool x_fits = (int64_t)a.T * p.row_chunks <= UINT32_MAX;
+    for (int m = 0; m < a.n_mats; ++m)
+        if (w_fits && unit_of(a.w[m], a.ldw[m]) < 16) a.w[m] = copy(a.w[m], a.ldw[m], a.rows);
+    if (tokens && x_fits && unit_of(a.x, a.ldx) < 16) a.x = reinterpret_cast<const int8_t*>(copy(a.x, a.ldx, a.T));
+    if (!p.n) return cudaSuccess;
+    const int sms = device_info().sm_count;
+    const bool few = p.n * most <= 512 * (int64_t)sms;
+    const int64_t per = few ? 256 : 512, want = (most + per - 1) / per, cap = 8 * sms / p.n;
+    const dim3 grid((unsigned)(want < cap ? want : cap), p.n);
+    return launch_dense(few ? k_pad_rows<1> : k_pad_rows<2>, grid, 256, 0, 1, s, p);
+}
+
 }  // namespace dense
 }  // namespace moe

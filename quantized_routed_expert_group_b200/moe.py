@@ -64,10 +64,12 @@ _SIGS = {
     "moe_block_dots": ([_vp, _i64, _int, _int, _vp, _int, _vp, _vp], _int),
     "moe_block_dots_routine": ([_vp, _i64, _int, _int, _vp, _int, _int, _vp, _vp], _int),
     "moe_quantize_act_token": ([_vp, _int, _i64, _int, _i64, _vp, _i64, _vp, _vp], _int),
-    "moe_int8_matmul": ([_vp, _i64, _vp, _int, _vp, _i64, _vp, _int, _int, _vp, _vp, _int, _i64, _vp, _vp], _int),
+    "moe_int8_forward_workspace_bytes": ([_int, _int, _int, _int], _sz),
+    "moe_int8_matmul": ([_vp, _i64, _vp, _int, _vp, _i64, _vp, _int, _int, _vp, _vp, _int, _i64, _vp, _vp, _sz, _vp],
+                        _int),
     "moe_gated_ffn": ([_vp, _i64, _vp, _int, _vp, _i64, _vp, _vp, _i64, _vp, _int, _int, _int, _vp, _int, _i64, _vp,
-                       _vp], _int),
-    "moe_int8_backward_workspace_bytes": ([_int, _int, _int, _int], _sz),
+                       _vp, _sz, _vp], _int),
+    "moe_int8_backward_workspace_bytes": ([_int, _int, _int, _int, _int], _sz),
     "moe_int8_matmul_backward": ([_vp, _int, _i64, _vp, _vp, _int, _vp, _i64, _vp, _int, _int, _vp, _i64, _vp, _vp,
                                   _vp, _sz, _vp], _int),
     "moe_gated_ffn_backward": ([_vp, _int, _i64, _vp, _vp, _int, _vp, _i64, _vp, _vp, _i64, _vp, _int, _int, _int,
@@ -456,6 +458,12 @@ def quantize_act_token(x: torch.Tensor, stream=None):
     return q, d
 
 
+def _room(n_mats: int, T: int, N: int, K: int, like: torch.Tensor):
+    """Workspace for rows off the 16-byte grid, where the products use one, and its size."""
+    size = lib().moe_int8_forward_workspace_bytes(n_mats, T, N, K) if K % 16 else 0
+    return (like.new_empty(size, dtype=torch.uint8), size) if size else (None, 0)
+
+
 def int8_matmul(xq: torch.Tensor, xd: torch.Tensor, w: torch.Tensor, s: torch.Tensor,
                 bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
                 out: torch.Tensor | None = None, save: bool = False, stream=None):
@@ -478,8 +486,10 @@ def int8_matmul(xq: torch.Tensor, xd: torch.Tensor, w: torch.Tensor, s: torch.Te
     else:
         y, ldo = out, _matrix(out, (out_dtype,), "out", T, N, dev)
     acc = xq.new_empty(T, N, dtype=torch.int32) if save else None
+    ws, size = _room(1, T, N, K, w)
     st = lib().moe_int8_matmul(xq.data_ptr(), ldx, xd_p, T, w.data_ptr(), ldw, s_p, N, K, bias_p, y.data_ptr(), dt,
-                               ldo, acc.data_ptr() if save else None, _raw_stream(dev))
+                               ldo, acc.data_ptr() if save else None, ws.data_ptr() if size else None, size,
+                               _raw_stream(dev))
     _check(st, "int8_matmul")
     return (y, acc) if save else y
 
@@ -506,7 +516,7 @@ def int8_matmul_backward(dy: torch.Tensor, acc: torch.Tensor | None, xd: torch.T
         db = s.new_empty(N)
     dt = _DTYPES[dy.dtype]
     dx = dy.new_empty(T, K)
-    size = lib().moe_int8_backward_workspace_bytes(1, T, N, dt)
+    size = lib().moe_int8_backward_workspace_bytes(1, T, N, K, dt)
     ws = w.new_empty(size, dtype=torch.uint8)
     st = lib().moe_int8_matmul_backward(dy.data_ptr(), dt, lddy, acc_p, xd_p, T, w.data_ptr(), ldw, s_p, N, K,
                                         dx.data_ptr(), K, None if ds is None else ds.data_ptr(),
@@ -538,8 +548,10 @@ def gated_ffn(xq: torch.Tensor, xd: torch.Tensor, w_gate: torch.Tensor, s_gate: 
     else:
         h, ldo = out, _matrix(out, (out_dtype,), "out", T, N, dev)
     acc = xq.new_empty(2, T, N, dtype=torch.int32) if save else None
+    ws, size = _room(2, T, N, K, w_gate)
     st = lib().moe_gated_ffn(xq.data_ptr(), ldx, xd_p, T, w_gate.data_ptr(), ldg, sg_p, w_up.data_ptr(), ldu, su_p, N,
-                             K, ac, h.data_ptr(), dt, ldo, acc.data_ptr() if save else None, _raw_stream(dev))
+                             K, ac, h.data_ptr(), dt, ldo, acc.data_ptr() if save else None,
+                             ws.data_ptr() if size else None, size, _raw_stream(dev))
     _check(st, "gated_ffn")
     return (h, acc) if save else h
 
@@ -564,7 +576,7 @@ def gated_ffn_backward(dh: torch.Tensor, acc: torch.Tensor, xd: torch.Tensor, w_
     dt, ac = _DTYPES[dh.dtype], _choice(act, _ACTS, "act")
     dx = dh.new_empty(T, K)
     dsg, dsu = s_gate.new_empty(N), s_up.new_empty(N)
-    size = lib().moe_int8_backward_workspace_bytes(2, T, N, dt)
+    size = lib().moe_int8_backward_workspace_bytes(2, T, N, K, dt)
     ws = w_gate.new_empty(size, dtype=torch.uint8)
     st = lib().moe_gated_ffn_backward(dh.data_ptr(), dt, lddh, acc_p, xd_p, T, w_gate.data_ptr(), ldg, sg_p,
                                       w_up.data_ptr(), ldu, su_p, N, K, ac, dx.data_ptr(), K, dsg.data_ptr(),

@@ -19,9 +19,9 @@ def L():
 
 
 MATMUL = dict(xq=A, ldx=64, xd=A, T=4, w=A, ldw=64, s=A, rows=32, cols=64, bias=None, out=A, dtype=0, ldo=32,
-              acc=None)
+              acc=None, ws=None, ws_bytes=0)
 GATED = dict(xq=A, ldx=64, xd=A, T=4, wg=A, ldg=64, sg=A, wu=A, ldu=64, su=A, rows=32, cols=64, act=0, out=A,
-             dtype=0, ldo=32, acc=None)
+             dtype=0, ldo=32, acc=None, ws=None, ws_bytes=0)
 MATMUL_B = dict(dy=A, dtype=0, lddy=32, acc=A, xd=A, T=4, w=A, ldw=64, s=A, rows=32, cols=64, dx=A, lddx=64, ds=A,
                 dbias=A, ws=A, ws_bytes=1 << 30)
 GATED_B = dict(dh=A, dtype=0, lddh=32, acc=A, xd=A, T=4, wg=A, ldg=64, sg=A, wu=A, ldu=64, su=A, rows=32, cols=64,
@@ -46,6 +46,8 @@ GATED_B = dict(dh=A, dtype=0, lddh=32, acc=A, xd=A, T=4, wg=A, ldg=64, sg=A, wu=
     ("moe_int8_matmul", MATMUL, dict(ldo=31), EINVAL),
     ("moe_int8_matmul", MATMUL, dict(bias=A + 1), EINVAL),
     ("moe_int8_matmul", MATMUL, dict(acc=A + 2), EINVAL),
+    ("moe_int8_matmul", MATMUL, dict(ws=A + 16), EINVAL),
+    ("moe_gated_ffn", GATED, dict(ws=A + 128, ws_bytes=64), EINVAL),
     ("moe_int8_matmul", MATMUL, dict(cols=131072, ldx=131072, ldw=131072), EUNSUPPORTED),
     ("moe_int8_matmul", MATMUL, dict(T=(1 << 28) + 1), EUNSUPPORTED),
     ("moe_int8_matmul", MATMUL, dict(T=0, xq=None, out=None, xd=None), 0),
@@ -107,11 +109,18 @@ def test_ffn_refusals(L):
 def test_workspace_sizes(L):
     lib = L.lib()
     for n_mats, dtype, planes in ((1, 0, 3), (2, 0, 3), (1, 1, 2), (2, 2, 2)):
-        n = lib.moe_int8_backward_workspace_bytes(n_mats, 300, 500, dtype)
+        n = lib.moe_int8_backward_workspace_bytes(n_mats, 300, 500, 64, dtype)
         assert n >= planes * 300 * n_mats * 512 + 300 * 8  # planes and row scales
-    assert lib.moe_int8_backward_workspace_bytes(1, 0, 8, 0) > 0
-    for bad in ((0, 4, 8, 0), (3, 4, 8, 0), (1, -1, 8, 0), (1, 4, 0, 0), (1, 4, 8, 5), (2, 4, 65536, 0)):
+    assert lib.moe_int8_backward_workspace_bytes(1, 0, 8, 64, 0) > 0
+    for bad in ((0, 4, 8, 64, 0), (3, 4, 8, 64, 0), (1, -1, 8, 64, 0), (1, 4, 0, 64, 0), (1, 4, 8, 64, 5),
+                (2, 4, 65536, 64, 0), (1, 4, 8, 0, 0)):
         assert lib.moe_int8_backward_workspace_bytes(*bad) == 0
+    # room for rows off the 16-byte grid, where copying them pays
+    room = lib.moe_int8_forward_workspace_bytes
+    assert room(1, 300, 3000, 1000) >= 3300 * 1008 and room(2, 300, 3000, 1000) >= 6300 * 1008
+    assert room(1, 300, 3000, 1008) == room(1, 16, 3000, 1000) == room(1, 300, 100, 100) == 0
+    assert room(0, 300, 3000, 1000) == room(1, 300, 3000, 131072) == room(1, -1, 3000, 1000) == 0
+    assert lib.moe_int8_backward_workspace_bytes(1, 4, 3000, 1000, 0) >= 3000 * 1008
     assert lib.moe_dense_ffn_workspace_bytes(4, 64, 32) >= 4 * (64 + 32 + 4 * 32 + 8)
     assert lib.moe_dense_ffn_workspace_bytes(-1, 64, 32) == 0
     assert lib.moe_dense_device_error(None, None) == EINVAL

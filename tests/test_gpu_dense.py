@@ -191,3 +191,40 @@ def test_strided_operands_and_results(T, offset, extra):
     (q, d), (q0, d0) = moe.quantize_act_token(xfv), moe.quantize_act_token(xf.cuda())
     assert torch.equal(q, q0) and torch.equal(d, d0)
     assert moe.dense_device_error() == 0
+
+
+@pytest.mark.parametrize("T,K,N", [(333, 1001, 777), (40, 4093, 1333), (300, 2050, 2809), (700, 3001, 1030),
+                                   (129, 8185, 8200), (17, 70001, 33)])
+def test_odd_rows_copied_or_as_they_lie(T, K, N):
+    """Rows of an odd length give the bits of the same rows at a stride of 16 bytes, with the
+    workspace that holds their copies, without one and with one that is too small."""
+    gen = torch.Generator().manual_seed(T + K + N)
+    xq = torch.randint(-127, 128, (T, K), generator=gen, dtype=torch.int8)
+    ws = [torch.randint(-127, 128, (N, K), generator=gen, dtype=torch.int8) for _ in range(2)]
+    xd, *ss = cuda(torch.rand(T, generator=gen), *(torch.rand(N, generator=gen) * 1e-3 for _ in range(2)))
+    dy = torch.randn((T, N), generator=gen).cuda()
+    pitch = (K + 15) // 16 * 16
+    even = [strided(t, 0, pitch, 99)[1] for t in (xq, *ws)]
+    odd = cuda(xq, *ws)
+
+    def run(x, wg, wu):
+        y, acc = moe.int8_matmul(x, xd, wg, ss[0], out_dtype=torch.bfloat16, save=True)
+        h, acc2 = moe.gated_ffn(x, xd, wg, ss[0], wu, ss[1], out_dtype=torch.float32, save=True)
+        dx, ds = moe.int8_matmul_backward(dy, acc, xd, wg, ss[0])[:2]
+        back = moe.gated_ffn_backward(dy.bfloat16(), acc2, xd, wg, ss[0], wu, ss[1])
+        return [y, acc, h, acc2, dx, ds, *back]
+
+    want = run(*even)
+    for i, (a, b) in enumerate(zip(run(*odd), want)):
+        assert torch.equal(a, b), i
+    lib, stream = moe.lib(), torch.cuda.current_stream().cuda_stream
+    need = lib.moe_int8_forward_workspace_bytes(2, T, N, K)
+    room = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for ptr, size in ((None, 0), (room.data_ptr(), need - 1), (room.data_ptr(), need)):
+        y, h = torch.empty_like(want[0]), torch.empty_like(want[2])
+        assert lib.moe_int8_matmul(odd[0].data_ptr(), K, xd.data_ptr(), T, odd[1].data_ptr(), K, ss[0].data_ptr(), N,
+                                   K, None, y.data_ptr(), 1, N, None, ptr, size, stream) == 0
+        assert lib.moe_gated_ffn(odd[0].data_ptr(), K, xd.data_ptr(), T, odd[1].data_ptr(), K, ss[0].data_ptr(),
+                                 odd[2].data_ptr(), K, ss[1].data_ptr(), N, K, 0, h.data_ptr(), 0, N, None, ptr, size,
+                                 stream) == 0
+        assert torch.equal(y, want[0]) and torch.equal(h, want[2])
