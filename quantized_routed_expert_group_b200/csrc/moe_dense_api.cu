@@ -43,12 +43,15 @@ static int check_matrix(const void* p, int dtype, int64_t ld, int cols) {
     return p && aligned(p, elem_size(dtype)) && ld >= cols ? MOE_OK : MOE_EINVAL;
 }
 
-// Copies of odd rows pay from about a megabyte on (333 x 1001 x 777: 12.0 -> 8.5 us;
-// 300 x 1000 x 500, 0.8 MB: 8.1 -> 8.7 us), and not for the few tokens that stream
-// the weights.
+// Copies of odd rows pay from 1.5 MB on: 333 x 1000 x 777 gated (1.9 MB) 17.9 ->
+// 10.5 us.  Below, the device saves less than the host spends on the launch (300 x
+// 1000 x 500 gated, 1.3 MB: 10.7 -> 8.5 us, and 3.5 us of the host), and the few
+// tokens that stream the weights gain nothing.
+constexpr size_t kCopyBytes = 3u << 19;
+
 static size_t forward_room(int n_mats, int T, int rows, int cols) {
     const size_t n = pad_bytes(n_mats, T, rows, cols);
-    return cols % 16 && T > kFewTokens && n >= 1u << 20 ? align256(n) : 0;
+    return cols % 16 && T > kFewTokens && n >= kCopyBytes ? align256(n) : 0;
 }
 
 struct BackwardLayout {
@@ -65,8 +68,8 @@ static BackwardLayout backward_layout(int n_mats, int T, int rows, int cols, int
     const size_t parts = n_mats == 2 ? grad_rows_grid(T) : T / 32 < kMaxDotChunks ? T / 32 : kMaxDotChunks;
     L.done = L.partials + align256(parts * 2 * rows * sizeof(float));
     L.room = L.done + (n_mats == 2 ? 0 : align256(col_dots_tiles(rows) * sizeof(int)));
-    // the weights alone; at every size measured (300 x 1000 x 500: 14.1 -> 12.8 us)
-    L.total = L.room + (cols % 16 ? align256(pad_bytes(n_mats, 0, rows, cols)) : 0);
+    const size_t n = pad_bytes(n_mats, 0, rows, cols);  // the weights alone
+    L.total = L.room + (cols % 16 && n >= kCopyBytes ? align256(n) : 0);
     return L;
 }
 

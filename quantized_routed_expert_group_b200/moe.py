@@ -8,6 +8,7 @@ if the CUDA library has not been built, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -458,9 +459,19 @@ def quantize_act_token(x: torch.Tensor, stream=None):
     return q, d
 
 
+@functools.lru_cache(maxsize=1024)
+def _room_bytes(n_mats: int, T: int, N: int, K: int) -> int:
+    return lib().moe_int8_forward_workspace_bytes(n_mats, T, N, K)
+
+
+@functools.lru_cache(maxsize=1024)
+def _backward_bytes(n_mats: int, T: int, N: int, K: int, dtype: int) -> int:
+    return lib().moe_int8_backward_workspace_bytes(n_mats, T, N, K, dtype)
+
+
 def _room(n_mats: int, T: int, N: int, K: int, like: torch.Tensor):
     """Workspace for rows off the 16-byte grid, where the products use one, and its size."""
-    size = lib().moe_int8_forward_workspace_bytes(n_mats, T, N, K) if K % 16 else 0
+    size = _room_bytes(n_mats, T, N, K) if K % 16 else 0
     return (like.new_empty(size, dtype=torch.uint8), size) if size else (None, 0)
 
 
@@ -516,7 +527,7 @@ def int8_matmul_backward(dy: torch.Tensor, acc: torch.Tensor | None, xd: torch.T
         db = s.new_empty(N)
     dt = _DTYPES[dy.dtype]
     dx = dy.new_empty(T, K)
-    size = lib().moe_int8_backward_workspace_bytes(1, T, N, K, dt)
+    size = _backward_bytes(1, T, N, K, dt)
     ws = w.new_empty(size, dtype=torch.uint8)
     st = lib().moe_int8_matmul_backward(dy.data_ptr(), dt, lddy, acc_p, xd_p, T, w.data_ptr(), ldw, s_p, N, K,
                                         dx.data_ptr(), K, None if ds is None else ds.data_ptr(),
@@ -576,7 +587,7 @@ def gated_ffn_backward(dh: torch.Tensor, acc: torch.Tensor, xd: torch.Tensor, w_
     dt, ac = _DTYPES[dh.dtype], _choice(act, _ACTS, "act")
     dx = dh.new_empty(T, K)
     dsg, dsu = s_gate.new_empty(N), s_up.new_empty(N)
-    size = lib().moe_int8_backward_workspace_bytes(2, T, N, K, dt)
+    size = _backward_bytes(2, T, N, K, dt)
     ws = w_gate.new_empty(size, dtype=torch.uint8)
     st = lib().moe_gated_ffn_backward(dh.data_ptr(), dt, lddh, acc_p, xd_p, T, w_gate.data_ptr(), ldg, sg_p,
                                       w_up.data_ptr(), ldu, su_p, N, K, ac, dx.data_ptr(), K, dsg.data_ptr(),
