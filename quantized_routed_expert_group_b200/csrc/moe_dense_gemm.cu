@@ -663,20 +663,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_columns(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld32(taddr, v); }
-__device__ __forceinline__ void tmem_ld_columns(uint32_t taddr, uint32_t (&v)[16]) { tmem_ld16(taddr, v); }
-
-// C values of each of a warp's 32 rows (a lane holds its row's columns n ..
-// n + C - 1) to rows t0 .. of [T][N] at n, through the warp's staging buffer: a row
-// is written by C * sizeof(V) / 16 neighbouring lanes, 16 bytes each, where out,
-// N and ld are multiples of that (vec), and by C lanes an element each elsewhere.
+// 32 values of each of a warp's 32 rows (a lane holds its row's columns n ..
+// n + 31) to rows t0 .. of [T][N] at n, through the warp's staging buffer: a row
+// is written by 32 * sizeof(V) / 16 neighbouring lanes, 16 bytes each, where out,
+// N and ld are multiples of that (vec), and by 32 lanes an element each elsewhere.
 // (Each lane storing its own odd row took 97 us in place of 38 at 2000 x 2049 x
 // 3001, gated.)
-template <typename V, typename W, int C>
-__device__ __forceinline__ void store_rows(V* out, int64_t ld, int64_t T, int N, int64_t t0, int n, const W (&v)[C],
-                                           int vec, uint8_t* stage, int lane) {
+template <typename V, typename W>
+__device__ __forceinline__ void store_rows32(V* out, int64_t ld, int64_t T, int N, int64_t t0, int n,
+                                             const W (&v)[32], int vec, uint8_t* stage, int lane) {
     static_assert(sizeof(V) == sizeof(W), "the same elements");
-    constexpr int kPieces = C * (int)sizeof(V) / 16, kPitch = 16 * kPieces + 16, kEach = 16 / (int)sizeof(V);
+    constexpr int kPieces = 32 * (int)sizeof(V) / 16, kPitch = 16 * kPieces + 16, kEach = 16 / (int)sizeof(V);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i)
         *reinterpret_cast<uint4*>(stage + lane * kPitch + 16 * i) = reinterpret_cast<const uint4*>(v)[i];
@@ -690,12 +687,12 @@ __device__ __forceinline__ void store_rows(V* out, int64_t ld, int64_t T, int N,
             const uint4 w = *reinterpret_cast<const uint4*>(stage + row * kPitch + 16 * piece);
             if (in && t0 + row < T) *reinterpret_cast<uint4*>(out + (t0 + row) * ld + n + piece * kEach) = w;
         }
-    } else if (n + lane % C < N) {
+    } else if (n + lane < N) {
         const int nr = (int)(T - t0 < 32 ? T - t0 : 32);
-        V* o = out + t0 * ld + n + lane % C;
+        V* o = out + t0 * ld + n + lane;
 #pragma unroll 8
-        for (int row = lane / C; row < nr; row += 32 / C)
-            o[row * ld] = *reinterpret_cast<const V*>(stage + row * kPitch + lane % C * (int)sizeof(V));
+        for (int row = 0; row < nr; ++row, o += ld)
+            *o = *reinterpret_cast<const V*>(stage + row * kPitch + lane * (int)sizeof(V));
     }
     __syncwarp();
 }
@@ -878,36 +875,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tc_fence_after_sync();
             const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 256 * buf + half * cols * P;
             if constexpr (MODE == kGated) {
-                // 32 channels at a time (16 where a unit has no more), turned in shared
-                // memory so that the stores run along the tokens' rows
+                // 32 channels at a time, turned in shared memory so that the stores run
+                // along the tokens' rows (a unit of 16 computes 16 idle ones: one code
+                // for both is faster than two)
                 uint8_t* stage = sm + kStages * kStage + (warp - 2) * kStageWarp;
                 const int64_t t0 = r0 - lane;
-                auto columns = [&](int c, auto width) {
-                    constexpr int C = decltype(width)::value;
-                    alignas(16) uint32_t g[C], u[C];
-                    tmem_ld_columns(tl + c, g);
-                    tmem_ld_columns(tl + un.nt + c, u);
+                const int end = (int)min((int64_t)p.rows, c0 + cols);
+                for (int c = 0; c < cols; c += 32) {
+                    uint32_t g[32], u[32];
+                    tmem_ld32(tl + c, g);
+                    tmem_ld32(tl + un.nt + c, u);
                     tmem_wait_ld();
                     const int n = (int)c0 + c;
                     if (p.acc) {
-                        store_rows(p.acc, p.rows, p.T, p.rows, t0, n, g, p.vec, stage, lane);
-                        store_rows(p.acc + p.T * (int64_t)p.rows, p.rows, p.T, p.rows, t0, n, u, p.vec, stage, lane);
+                        store_rows32(p.acc, p.rows, p.T, end, t0, n, g, p.vec, stage, lane);
+                        store_rows32(p.acc + p.T * (int64_t)p.rows, p.rows, p.T, end, t0, n, u, p.vec, stage, lane);
                     }
-                    alignas(16) OT h[C];
+                    alignas(16) OT h[32];
                     with_act(p.act, [&](auto act) {
 #pragma unroll
-                        for (int j = 0; j < C; ++j) {
+                        for (int j = 0; j < 32; ++j) {
                             const RowScale sc = ts[c + j];
                             h[j] = from_f32<OT>(act_value<decltype(act)::value>((float)(int)g[j] * (sa * sc.a)) *
                                                 ((float)(int)u[j] * (sa * sc.b)));
                         }
                     });
-                    store_rows(static_cast<OT*>(p.out), p.ldo, p.T, p.rows, t0, n, h, p.vec, stage, lane);
-                };
-                if (cols % 32 == 0) {
-                    for (int c = 0; c < cols; c += 32) columns(c, std::integral_constant<int, 32>{});
-                } else {
-                    for (int c = 0; c < cols; c += 16) columns(c, std::integral_constant<int, 16>{});
+                    store_rows32(static_cast<OT*>(p.out), p.ldo, p.T, end, t0, n, h, p.vec, stage, lane);
                 }
             } else {
                 const int nv = (int)min((int64_t)cols, p.T - c0);
