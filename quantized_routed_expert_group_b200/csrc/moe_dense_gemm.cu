@@ -256,7 +256,9 @@ __device__ __forceinline__ void emit_channel(const ChannelOut& o, const int (&v)
 // One 128-channel x nt-token tile per cluster; the CTAs of a cluster split the
 // contraction and add their integer sums through distributed shared memory
 // (exact, so the split changes no bit).  Every wait is bounded by the global
-// timer and records kErrTimeout.
+// timer and records kErrTimeout.  Bound by latency: the ring's fill, the tile's
+// epilogue and the cluster's barriers (333 x 1008 x 784: 5.8 us; with rows of 1000
+// codes, loaded by threads, 8.9).
 template <int MODE, int P, typename OT>
 __global__ void __launch_bounds__(kDirectThreads)
     k_dense_tile(const __grid_constant__ CUtensorMap wmap0, const __grid_constant__ CUtensorMap wmap1,
@@ -538,6 +540,10 @@ __global__ void __launch_bounds__(kDirectThreads)
 //     is a channel, and a warp's stores run along a token's row
 //   gated: rows = 256 tokens, columns = 128 gate and 128 up channels (one half
 //     from each CTA), so that a lane holds a token's g and u of one channel
+// Bound by the tensor pipe and the power limit: 4096 x 6144 x 6144 (bf16 results)
+// 97 us, 3.19 POP/s, the pipe busy in 78 % of all cycles at 1.65 GHz; gated 4096 x
+// 6144 x 2048 66 us, 3.12 POP/s, 72 %; the rest is the last round's remainder and
+// the last tile's epilogue.
 constexpr int kPairThreads = 320;  // producer warp, MMA warp, eight epilogue warps
 // (the gated kernel gives a stage's room to its epilogue's staging)
 template <int MODE>
