@@ -647,12 +647,11 @@ cudaError_t launch_col_dots(const GradRowsArgs& a, float* ds, float* dbias, cuda
 }
 
 // ---------------------------------------------------------------------------
-// Rows of codes off the 16-byte grid to rows on it (bytes past a row's end are
-// left: the products read rows by their length).  Up to three matrices a launch,
-// one for each blockIdx.y, in chunks of 16 bytes, EACH of them under way a thread
-// (1 while the threads find room on the device at once).  Bound by latency at a
-// few megabytes, by memory beyond: 2000 x 2049 codes and 3001 x 2049, 20 MB of
-// traffic, 5 us.
+// Rows of codes off the 16-byte grid to rows on it, zeros past a row's end.  Up to
+// three matrices a launch, one for each blockIdx.y, in chunks of 16 bytes, EACH of
+// them under way a thread (1 while the threads find room on the device at once).
+// Bound by latency at a few megabytes, by memory beyond: 2000 x 2049 codes and
+// 3001 x 2049, 20 MB of traffic, 5 us.
 // ---------------------------------------------------------------------------
 struct PadParams {
     const uint8_t* src[3];

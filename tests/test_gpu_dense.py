@@ -15,7 +15,7 @@ DT = dh.DTYPES
 SIZES = [(24, 1040, 300), (32, 272, 65), (20, 999, 77), (1, 1, 1), (1, 16, 1), (1, 6144, 300), (2, 127, 5), (3, 129, 130), (4, 512, 128), (5, 2048, 257),
          (16, 1000, 77), (17, 128, 384), (33, 100, 64), (64, 1040, 129), (65, 36, 127), (128, 256, 128),
          (129, 260, 131), (300, 1000, 500), (257, 1536, 640)]
-LARGE = [(700, 2048, 1504), (1030, 1024, 528), (513, 272, 1032), (256, 16, 16), (2500, 128, 4000), (4000, 1040, 3120), (40, 64, 6200), (30, 48, 7001), (21, 32, 16500), (600, 64, 8192), (1500, 64, 40), (3000, 48, 333)]
+LARGE = [(333, 1001, 777), (640, 1003, 1501), (700, 2048, 1504), (1030, 1024, 528), (513, 272, 1032), (256, 16, 16), (2500, 128, 4000), (4000, 1040, 3120), (40, 64, 6200), (30, 48, 7001), (21, 32, 16500), (600, 64, 8192), (1500, 64, 40), (3000, 48, 333)]
 
 
 def cuda(*ts):
