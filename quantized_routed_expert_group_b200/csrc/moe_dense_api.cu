@@ -44,7 +44,7 @@ static int check_matrix(const void* p, int dtype, int64_t ld, int cols) {
 }
 
 // Copies of odd rows pay from 1.5 MB on: 333 x 1000 x 777 gated (1.9 MB) 17.9 ->
-// 10.5 us.  Below, the device saves less than the host spends on the launch (300 x
+// 11.4 us.  Below, the device saves less than the host spends on the launch (300 x
 // 1000 x 500 gated, 1.3 MB: 10.7 -> 8.5 us, and 3.5 us of the host), and the few
 // tokens that stream the weights gain nothing.
 constexpr size_t kCopyBytes = 3u << 19;
@@ -362,7 +362,8 @@ MOE_API int moe_dense_ffn(const void* x, int dtype, int64_t ldx, int T, int hidd
     st = moe_quantize_act_token(x, dtype, T, hidden, ldx, xq, L.ldx, xd, stream);
     if (!st)
         st = moe_gated_ffn(xq, L.ldx, xd, T, experts->w_gate, hidden, experts->s_gate, experts->w_up, hidden,
-                           experts->s_up, inter, hidden, act, h, MOE_F32, L.ldh, nullptr, ws + L.room, L.total - L.room, stream);
+                           experts->s_up, inter, hidden, act, h, MOE_F32, L.ldh, nullptr, ws + L.room, L.total - L.room,
+                           stream);
     if (!st) st = moe_quantize_act_token(h, MOE_F32, T, inter, L.ldh, hq, L.ldh, hd, stream);
     if (!st)
         st = moe_int8_matmul(hq, L.ldh, hd, T, experts->w_down, inter, experts->s_down, hidden, inter, nullptr, out,

@@ -882,8 +882,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16) + 256 * buf + half * cols * P;
             if constexpr (MODE == kGated) {
                 // 32 channels at a time, turned in shared memory so that the stores run
-                // along the tokens' rows (a unit of 16 computes 16 idle ones: one code
-                // for both is faster than two)
+                // along the tokens' rows.  A unit of 16 channels computes 16 idle ones: a
+                // form of its own saved 0.9 of 11.4 us at 333 x 1000 x 777 and doubled
+                // this code.
                 uint8_t* stage = sm + kStages * kStage + (warp - 2) * kStageWarp;
                 const int64_t t0 = r0 - lane;
                 const int end = (int)min((int64_t)p.rows, c0 + cols);
