@@ -429,10 +429,11 @@ size_t moe_int8_backward_workspace_bytes(int n_mats, int T, int rows, int cols, 
  *   dx[t][k] = sum_n dy[t][n] s[n] w[n][k]  (type dtype)
  *   ds[n] = sum_t dy[t][n] xd[t] acc[t][n],  dbias[n] = sum_t dy[t][n]  (fp32)
  * ds and dbias may be NULL; acc and xd are needed for ds only (NULL
- * otherwise).  The rows dy s are written as fixed-point numbers relative to the
- * row's largest, 16 bits for 16-bit types and 24 for fp32, and multiplied
- * exactly: an element is off by at most 2^-16 (2^-24) of the largest.  A row
- * with an infinity or a NaN gives NaN in its row of dx.
+ * otherwise).  The rows v = dy s are written as fixed-point numbers relative to
+ * the row's largest magnitude m and multiplied exactly: an element is off by at
+ * most 2^-22 |v| (fp32 roundings) and m / (2 D), D = 8355600 for 16-bit types
+ * (2^-24 m) and 2139060224 for fp32 (2^-32 m).  A row with an infinity or a NaN
+ * gives NaN in its row of dx.
  * workspace: >= moe_int8_backward_workspace_bytes(1, T, rows, cols, dtype) bytes,
  * 256-byte aligned; nothing in it is kept between calls. */
 int moe_int8_matmul_backward(const void *dy, int dtype, int64_t lddy, const int32_t *acc, const float *xd, int T,

@@ -197,19 +197,24 @@ __device__ __forceinline__ void store_bytes(int8_t* p, const int (&c)[VEC], uint
 
 // ---------------------------------------------------------------------------
 // Fixed-point planes of a gradient row.  A row v with m = max|v| is written as
-// the integers round(v D / m) of P signed base-256 digits, D = 32639 for P = 2
-// (127 in both digits) and 8355600 for P = 3 (some hundred below 127 in all
-// three, so that the product's rounding never lifts the top digit), so that
+// the integers round(v D / m) of P signed base-256 digits, D = 8355600 for P = 3
+// and 2139060224 for P = 4 (a little below 127 in all digits, so that the
+// product's rounding never lifts the top one), so that
 //   sum_n v_n w_n = (m / D) sum_p 256^p (digit_p . w)
 // runs as P int8 products against the packed weight rows as they lie, each
-// exact in int32.  The only rounding is the one to the row's fixed point: at
-// most m / (2 D) for an element (m 2^-16 for P = 2, m 2^-24 for P = 3).
-// Two planes serve 16-bit gradients (bf16 keeps 8 significant bits, fp16 11,
-// and the sum's error stays below half a step of the result), three fp32.
+// exact in int32.  v D / m rounds as fp32 numbers do (the multiplier and the
+// product: 2^-23 of v), and to the fixed point, by at most m / (2 D): m 2^-24
+// for P = 3, m 2^-32 for P = 4.  That second part is what a row of a wide range
+// can lose: its elements far below m.  16-bit gradients have three planes: N
+// such roundings stay below their result's own where the row has one element
+// far above the others (a softmax less its target over 128,256 rows: 2^-13 of
+// sum |v w|; two planes, 16 bits, lost a fifth of dx there).  fp32 gradients have
+// four, which keep an element's 24 bits down to m / 128 and leave less than an
+// fp32 sum's own rounding over 131,071 of them.
 // ---------------------------------------------------------------------------
-constexpr int planes_of(int dtype) { return dtype == MOE_F32 ? 3 : 2; }
+constexpr int planes_of(int dtype) { return dtype == MOE_F32 ? 4 : 3; }
 template <int P>
-constexpr float kPlaneMax = P == 2 ? 32639.0f : 8355600.0f;
+constexpr float kPlaneMax = P == 3 ? 8355600.0f : 2139060224.0f;
 
 // The planes of 16 tokens lie together, [T / 16][P][16] rows, so that a tile's
 // tokens are one box of memory whatever P is.

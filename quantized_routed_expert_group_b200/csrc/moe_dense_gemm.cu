@@ -988,7 +988,7 @@ static TilePlan plan_tile(int T, int tiles_n, int steps) {
     const ClusterTable& fit = clusters_at_once();
     TilePlan best{};
     double least = 1e30;
-    for (int nt = 16; nt <= (P == 3 ? 64 : 128); nt *= 2) {
+    for (int nt = 16; nt <= (MODE == kGrad ? 64 : 128); nt *= 2) {
         const int64_t tiles = (int64_t)tiles_n * ((T + nt - 1) / nt);
         const int cols = kV * nt, stage = kA * kTileRows * kStageK + P * nt * kStageK;
         const int tmem = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
@@ -1008,7 +1008,7 @@ static TilePlan plan_tile(int T, int tiles_n, int steps) {
             const int64_t rounds = (tiles + at_once - 1) / at_once;
             const double ctas = (double)(tiles < at_once ? tiles : at_once) * split;
             const double share = ctas > sms ? ctas / sms : 1.0;  // CTAs that share an SM
-            const double k = kV == 1 ? 1.0 : kV == 2 ? 1.7 : 2.4;
+            const double k = kV == 1 ? 1.0 : kV == 2 ? 1.7 : kV == 3 ? 2.4 : 3.1;
             const double end = split == 1 ? 1.5 + 0.023 * nt * k : 0.3 + (0.016 + 0.045 / split) * nt * k;
             const double stage_us = MODE == kGated ? 0.3 : MODE == kGrad ? 0.24 : 0.16;
             const double us = 5.0 + rounds * share * (per_cta * stage_us + end);
@@ -1092,7 +1092,7 @@ static cudaError_t run_tile(const GemmArgs& a, const TilePlan& plan, cudaStream_
 
 // Columns of a pair's tile (channels of the gated block, tokens elsewhere).
 template <int MODE, int P>
-constexpr int pair_columns = MODE == kGated ? 128 : MODE == kMatmul ? 256 : P == 2 ? 128 : 64;
+constexpr int pair_columns = MODE == kGated ? 128 : MODE == kMatmul ? 256 : 64;
 
 struct PairPlan {
     int tiles_r, parts;
@@ -1114,7 +1114,7 @@ static PairPlan plan_pair(int T, int out_rows, int steps) {
     const int64_t rest = tiles - p.whole;
     p.parts = 1;
     double end = rest ? 0.27 * steps + 4.0 : 4.0;
-    for (int q = 2; rest && q <= (P == 3 ? 2 : 4); q *= 2) {
+    for (int q = 2; rest && q <= (MODE == kGrad ? 2 : 4); q *= 2) {
         const double cost = (double)((rest * q + pairs - 1) / pairs) * steps * (q == 2 ? 0.24 : 0.235) + (q == 2 ? 1.5 : 1.0);
         if (cost < end) {
             end = cost;

@@ -188,22 +188,20 @@ __device__ __forceinline__ void grad_cols(const GradRowsParams& p, const GradIn<
 
 // The digits of VEC values into the row's planes.  Adding 128 to each of the
 // lower digits' places turns the signed digits into the bytes of one integer,
-// off by their top bit.  Two planes' integers are read off the mantissa of a
-// sum with 1.5 * 2^23 (one fused multiply-add, where the conversion has a
-// quarter of its rate); three planes' are too large for that.
+// off by their top bit (four planes: modulo 2^32).
 template <int P, int VEC>
 __device__ __forceinline__ void store_planes(const GradRowsParams& p, int64_t t, int m, int c, int mats, float mult,
                                              const float (&v)[VEC]) {
     int r[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
-        r[i] = P == 2 ? __float_as_int(fmaf(v[i], mult, 12582912.0f)) + (0x8080 - 0x4B400000)
-                      : __float2int_rn(v[i] * mult) + 0x808080;
+        r[i] = (int)((uint32_t)__float2int_rn(v[i] * mult) + (P == 3 ? 0x808080u : 0x80808080u));
     const int64_t row = mats * p.pitch;
     int8_t* o = p.planes + plane_row<P>(t) * row + m * p.pitch + c;
     store_bytes<VEC, 0>(o, r, 0x80808080u);
     store_bytes<VEC, 1>(o + kPlaneGroup * row, r, 0x80808080u);
-    if constexpr (P == 3) store_bytes<VEC, 2>(o + 2 * kPlaneGroup * row, r, 0x80808080u);
+    store_bytes<VEC, 2>(o + 2 * kPlaneGroup * row, r, 0x80808080u);
+    if constexpr (P == 4) store_bytes<VEC, 3>(o + 3 * kPlaneGroup * row, r, 0x80808080u);
 }
 
 template <int VEC>
