@@ -294,12 +294,16 @@ __global__ void __launch_bounds__(512, 2) k_grad_rows(const GradRowsParams p) {
 // ds[c] = sum_t dy xd acc, dbias[c] = sum_t dy.  A CTA takes 32 VEC columns of a
 // chunk of the rows, a row for each of its warps at a time, four of them under
 // way; its sums go to the partials, and the CTA that finishes a column tile last
-// joins the chunks' in their order, in fp64 (so the result does not depend on
-// which one that is; k_grad_rows zeroed the tiles' counters).
+// joins the chunks' in their order (so the result does not depend on which one
+// that is; k_grad_rows zeroed the tiles' counters).  A warp adds kSumRows rows in
+// fp32 and those sums in fp64, as are the warps' and the chunks', so that the error
+// is that of 32 additions whatever T is (one fp32 sum a thread: 1e-4 at 60,000
+// tokens of one sign).
 // It runs under the gradient's product, which leaves the memory idle: 256
-// threads and 9 KB of shared memory fit beside a pair's CTA.  It waits for that
+// threads and 8 KB of shared memory fit beside a pair's CTA.  It waits for that
 // product's end last, so that whatever follows finds both done.
 constexpr int kDotsWarps = 8;
+constexpr int kSumRows = 32;
 
 struct ColDotsParams {
     const void* dy;
@@ -316,16 +320,32 @@ struct ColDotsParams {
 template <int DT, int VEC>
 __global__ void __launch_bounds__(32 * kDotsWarps, 4) k_col_dots(const ColDotsParams p) {
     using T = typename Elem<DT>::T;
-    __shared__ float sh[kDotsWarps][2][32 * VEC];
+    __shared__ double sh[kDotsWarps][32 * VEC];
     __shared__ int last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tile = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
     const int c = tile * 32 * VEC + lane * VEC;
     const int64_t r1 = (int64_t)p.T * (chunk + 1) / p.chunks;
-    float sum[2][VEC] = {};
+    // fp64 sums of ds wait in shared memory (a slot for each thread and column),
+    // those of dbias in registers: with both in registers a CTA takes 80 a thread
+    // and finds no room beside a pair (157 against 108 us of the product's training
+    // step, 2048 x 2048 x 6144)
+    double total[VEC] = {};
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sh[warp][32 * i + lane] = 0.0;
     if (c < p.N) {
         const T* dy = static_cast<const T*>(p.dy) + c;
         const int32_t* acc = p.acc + c;
+        float sum[2][VEC] = {};
+        auto flush = [&] {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                sh[warp][32 * i + lane] += (double)sum[0][i];
+                total[i] += (double)sum[1][i];
+                sum[0][i] = sum[1][i] = 0.0f;
+            }
+        };
+        int held = 0;
         for (int64_t t = (int64_t)p.T * chunk / p.chunks + warp; t < r1; t += 4 * kDotsWarps) {
             Raw<T, VEC> d[4];
             Raw<int32_t, VEC> a[4];
@@ -341,6 +361,11 @@ __global__ void __launch_bounds__(32 * kDotsWarps, 4) k_col_dots(const ColDotsPa
                     }
                 }
             }
+            if (held == kSumRows) {
+                flush();
+                held = 0;
+            }
+            held += 4;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (t + k * kDotsWarps < r1)
@@ -351,21 +376,24 @@ __global__ void __launch_bounds__(32 * kDotsWarps, 4) k_col_dots(const ColDotsPa
                         sum[1][i] += v;
                     }
         }
+        flush();
     }
+    for (int m = 0; m < 2; ++m) {
+        if (m) {
+            __syncthreads();
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) sh[warp][m][lane * VEC + i] = sum[m][i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * 32 * VEC; i += 32 * kDotsWarps) {
-        const int m = i / (32 * VEC), col = tile * 32 * VEC + i % (32 * VEC);
-        if (col >= p.N) continue;
-        float a = 0.0f;
-        for (int w = 0; w < kDotsWarps; ++w) a += sh[w][m][i % (32 * VEC)];
-        if (p.chunks == 1) {
-            if (float* out = m ? p.dbias : p.ds) out[col] = a;
-        } else {
-            p.partials[((int64_t)chunk * 2 + m) * p.N + col] = a;
+            for (int i = 0; i < VEC; ++i) sh[warp][32 * i + lane] = total[i];
+        }
+        __syncthreads();
+        const int i = threadIdx.x, col = tile * 32 * VEC + i % 32 * VEC + i / 32;
+        if (i < 32 * VEC && col < p.N) {
+            double a = 0.0;
+            for (int w = 0; w < kDotsWarps; ++w) a += sh[w][i];
+            if (p.chunks == 1) {
+                if (float* out = m ? p.dbias : p.ds) out[col] = (float)a;
+            } else {
+                p.partials[((int64_t)chunk * 2 + m) * p.N + col] = (float)a;
+            }
         }
     }
     if (p.chunks > 1) {

@@ -116,3 +116,25 @@ def test_gated_backward_of_a_softmax_with_a_loud_channel(T, K, N, act, dtype):
     check_dx("dx", got[0], [dg * ss[0].double(), du * ss[1].double()], [eg * ss[0].double(), eu * ss[1].double()], ws,
              dtype)
     assert moe.dense_device_error() == 0
+
+
+# columns that leave one CTA the whole batch: many of them, and an odd number
+@pytest.mark.parametrize("T,N", [(20000, 9600), (60000, 2401), (70000, 33), (3000, 640)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_matmul_column_sums_of_a_long_batch(T, N, dtype):
+    """ds and dbias over batches of one sign, each column's terms alike, so that a long fp32 sum
+    would round the same way at every step.  Bounds: a term rounds three times, 32 of them are
+    summed in fp32, what follows is in fp64 but for one rounding a chunk and one of the result:
+    (3 + 31 + 2) u of the terms' sum."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    K = 16
+    dy = (torch.rand(N, generator=gen, device="cuda") + 0.1).to(DT[dtype]).expand(T, N).contiguous()
+    acc = torch.randint(1, 200_000, (N,), generator=gen, device="cuda", dtype=torch.int32).expand(T, N).contiguous()
+    xd = torch.full((T,), 0.0123, device="cuda")
+    w = torch.randint(-127, 128, (N, K), generator=gen, device="cuda", dtype=torch.int8)
+    s = torch.rand(N, generator=gen, device="cuda")
+    _, ds, db = moe.int8_matmul_backward(dy, acc, xd, w, s, bias_grad=True)
+    want = T * dy[0].double() * xd[0].double() * acc[0].double()
+    dh.check("ds", ds, want.cpu(), 36 * dh.U * want.cpu())
+    want = T * dy[0].double()
+    dh.check("dbias", db, want.cpu(), 36 * dh.U * want.cpu())
