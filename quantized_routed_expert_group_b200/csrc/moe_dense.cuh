@@ -411,10 +411,10 @@ struct GradRowsArgs {
     int8_t* planes;  // [plane_rows(P, T)][n_mats * pitch]
     int64_t pitch;
     RowScale* scale;   // [T]
-    float* partials;   // column sums: gated [grid][2][N]; one matrix [chunks][2][N]
+    float* partials;   // column sums: gated [grad_rows_parts][2][N]; one matrix [chunks][2][N]
     int* done;         // one matrix: counters of the column sums' tiles
 };
-int grad_rows_grid(int T);
+int64_t grad_rows_parts(int T);     // gated: partial sums of a column, at most
 constexpr int kMaxDotChunks = 64;  // row chunks of one matrix's column sums
 int col_dots_tiles(int N);         // their counters, at most
 // n_part: gated, how many partial sums of each column there are.

@@ -65,7 +65,7 @@ static BackwardLayout backward_layout(int n_mats, int T, int rows, int cols, int
     L.planes = 0;
     L.scale = align256((size_t)plane_rows(planes_of(dtype), T) * n_mats * L.pitch);
     L.partials = L.scale + align256((size_t)T * sizeof(RowScale));
-    const size_t parts = n_mats == 2 ? grad_rows_grid(T) : T / 32 < kMaxDotChunks ? T / 32 : kMaxDotChunks;
+    const size_t parts = n_mats == 2 ? (size_t)grad_rows_parts(T) : T / 32 < kMaxDotChunks ? T / 32 : kMaxDotChunks;
     L.done = L.partials + align256(parts * 2 * rows * sizeof(float));
     L.room = L.done + (n_mats == 2 ? 0 : align256(col_dots_tiles(rows) * sizeof(int)));
     const size_t n = pad_bytes(n_mats, 0, rows, cols);  // the weights alone

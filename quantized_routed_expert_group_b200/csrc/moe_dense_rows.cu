@@ -132,9 +132,10 @@ cudaError_t launch_quantize_token(const void* x, int dtype, int64_t rows, int co
 // and du s_u; column sums of dg xd acc_g and du xd acc_u, for which the
 // derivative would have to be formed again.  A CTA takes rows blockIdx.x,
 // + gridDim.x, ...; a thread owns the same columns in each of them, so it keeps
-// their column sums in registers and writes one partial sum a column and CTA,
-// which k_col_sums adds in CTA order (a fixed grid, no atomics: the sums do not
-// depend on timing).  Both matrices' values share the row's fixed point, so that
+// their column sums in registers and writes a partial sum a column for every
+// kSumRows of its rows, which k_col_sums adds in fp64 in a fixed order (a fixed
+// grid, no atomics: the sums do not depend on timing, and their error is that of
+// kSumRows additions whatever T is).  Both matrices' values share the row's fixed point, so that
 // their products add up in one accumulator.
 // ---------------------------------------------------------------------------
 struct GradRowsParams {
@@ -147,11 +148,13 @@ struct GradRowsParams {
     int8_t* planes;
     int64_t pitch;
     RowScale* scale;
-    float* partials;
+    float* partials;  // gated: [slots][grid][2][N]
+    int slots;        // gated: partial sums that a CTA writes
     int* done;  // one matrix: counters of k_col_dots, zeroed here
     bool bulk;  // rows of dy and acc start and end on 16 bytes
 };
 constexpr int kRowsAhead = 3;
+constexpr int kSumRows = 32;  // rows of a column sum in fp32
 constexpr int kMats = 2;  // gate and up
 
 // What VEC columns of a row read.
@@ -303,7 +306,6 @@ __global__ void __launch_bounds__(512, 2) k_grad_rows(const GradRowsParams p) {
 // threads and 8 KB of shared memory fit beside a pair's CTA.  It waits for that
 // product's end last, so that whatever follows finds both done.
 constexpr int kDotsWarps = 8;
-constexpr int kSumRows = 32;
 
 struct ColDotsParams {
     const void* dy;
@@ -436,6 +438,21 @@ __global__ void __launch_bounds__(VEC == 1 ? 1024 : 512) k_gated_rows(const Grad
 #pragma unroll
         for (int i = 0; i < VEC; ++i) sum[j][0][i] = sum[j][1][i] = 0.0f;
     auto col = [&](int j) { return (int)(threadIdx.x + j * blockDim.x) * VEC; };
+    float* part = p.partials + (int64_t)blockIdx.x * 2 * p.N;
+    auto flush = [&] {  // the column sums so far to the next slot
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            if (col(j) < p.N)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        part[(int64_t)k * p.N + col(j) + i] = sum[j][k][i];
+                        sum[j][k][i] = 0.0f;
+                    }
+        part += (int64_t)gridDim.x * 2 * p.N;
+    };
+    int held = 0, slot = 0;
     auto fetch = [&](int64_t t) {
         xd_next = p.xd[t];
 #pragma unroll
@@ -462,6 +479,12 @@ __global__ void __launch_bounds__(VEC == 1 ? 1024 : 512) k_gated_rows(const Grad
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
         const float xd = xd_next;
         ahead(t + (int64_t)(kRowsAhead + 1) * gridDim.x);
+        if (held == kSumRows) {
+            flush();
+            held = 0;
+            ++slot;
+        }
+        ++held;
         float v[NJ][kMats][VEC];
         float peak = 0.0f;
         with_act(p.act, [&](auto act) {
@@ -491,14 +514,7 @@ __global__ void __launch_bounds__(VEC == 1 ? 1024 : 512) k_gated_rows(const Grad
 #pragma unroll
                 for (int k = 0; k < kMats; ++k) store_planes<P, VEC>(p, t, k, col(j), kMats, mult, v[j][k]);
     }
-    float* part = p.partials + (int64_t)blockIdx.x * 2 * p.N;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-        if (col(j) < p.N)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) part[(int64_t)k * p.N + col(j) + i] = sum[j][k][i];
+    for (; slot < p.slots; ++slot) flush();  // (the last may be one row short of a sum: zeros)
 }
 
 // Rows of any length: the values are computed twice and the column sums kept
@@ -510,6 +526,7 @@ __global__ void __launch_bounds__(1024) k_gated_rows_long(const GradRowsParams p
     pdl_wait();
     pdl_launch_dependents();
     float* part = p.partials + (int64_t)blockIdx.x * 2 * p.N;
+    int held = 0, slot = 0;
     auto column = [&](int64_t t, int c, float xd, float (&v)[kMats][1], float (&sum)[2][1]) {
         GradIn<DT, 1> in;
         Raw<float, 1> sc[kMats];
@@ -521,14 +538,20 @@ __global__ void __launch_bounds__(1024) k_gated_rows_long(const GradRowsParams p
     int buf = 0;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, buf ^= 1) {
         const float xd = p.xd[t];
+        if (held == kSumRows) {
+            part += (int64_t)gridDim.x * 2 * p.N;
+            held = 0;
+            ++slot;
+        }
         float peak = 0.0f;
         for (int c = threadIdx.x; c < p.N; c += blockDim.x) {
             float v[kMats][1], sum[2][1];
-            for (int k = 0; k < 2; ++k) sum[k][0] = t == blockIdx.x ? 0.0f : part[(int64_t)k * p.N + c];
+            for (int k = 0; k < 2; ++k) sum[k][0] = held == 0 ? 0.0f : part[(int64_t)k * p.N + c];
             column(t, c, xd, v, sum);
             peak_of<1>(v, peak);
             for (int k = 0; k < 2; ++k) part[(int64_t)k * p.N + c] = sum[k][0];
         }
+        ++held;
         float lift;
         RowScale scale;
         const float mult = fixed_point<P>(block_max_bits(__float_as_uint(fabsf(peak)), sh, buf), lift, scale);
@@ -542,9 +565,14 @@ __global__ void __launch_bounds__(1024) k_gated_rows_long(const GradRowsParams p
             }
         }
     }
+    while (++slot < p.slots) {  // (at most one row short of another sum: zeros)
+        part += (int64_t)gridDim.x * 2 * p.N;
+        for (int c = threadIdx.x; c < p.N; c += blockDim.x)
+            for (int k = 0; k < 2; ++k) part[(int64_t)k * p.N + c] = 0.0f;
+    }
 }
 
-// out[c] = sum over the CTAs' partial sums, 32 columns a CTA: each of its 8
+// out[c] = sum over the partial sums, 32 columns a CTA: each of its 8
 // warps adds every 8th partial in fp64, then the warps' sums are added in order.
 // It runs under the gradient's product (small CTAs, no shared memory to speak
 // of), whose end it waits for last, so that whatever follows finds both done.
@@ -575,15 +603,31 @@ cudaError_t launch_col_sums(const float* partials, int n_part, int N, float* out
     return launch_dense(k_col_sums, 2 * tiles, 256, 0, 1, s, partials, n_part, N, out0, out1);
 }
 
-// CTAs of the gradient row kernel: a fixed grid (the column sums' order is the
-// same from call to call), at most two an SM.
-int grad_rows_grid(int T) {
-    const int most = 2 * device_info().sm_count;
+// CTAs of the gated gradient row kernel: a fixed grid (the column sums' order is
+// the same from call to call), at most per_sm (one or two) an SM; and the
+// partial sums that each of them writes.
+static int grad_rows_grid(int T, int per_sm) {
+    const int most = per_sm * device_info().sm_count;
     return T < most ? T : most;
 }
 
+static int grad_rows_slots(int T, int grid) {
+    const int rows = (T + grid - 1) / grid;
+    return (rows + kSumRows - 1) / kSumRows;
+}
+
+int64_t grad_rows_parts(int T) {
+    int64_t most = 0;
+    for (int per_sm = 1; T > 0 && per_sm <= 2; ++per_sm) {
+        const int grid = grad_rows_grid(T, per_sm);
+        const int64_t n = (int64_t)grid * grad_rows_slots(T, grid);
+        most = n > most ? n : most;
+    }
+    return most;
+}
+
 template <int DT>
-static cudaError_t grad_rows(const GradRowsArgs& a, GradRowsParams p, int& grid, cudaStream_t s) {
+static cudaError_t grad_rows(const GradRowsArgs& a, GradRowsParams p, int& n_part, cudaStream_t s) {
     const size_t vb = 4 * sizeof(typename Elem<DT>::T);
     bool vec = reinterpret_cast<uintptr_t>(a.dy) % vb == 0 && a.lddy % 4 == 0 && a.N % 4 == 0 &&
                reinterpret_cast<uintptr_t>(a.acc) % 16 == 0;
@@ -596,11 +640,11 @@ static cudaError_t grad_rows(const GradRowsArgs& a, GradRowsParams p, int& grid,
     // columns: 123.0 against 125.8 us of the training step at 2048 tokens).
     const int per = vec ? (groups <= 2 * 512 ? 2 : 4) : (groups <= 512 ? 1 : 4);
     const int threads = (groups + 32 * per - 1) / (32 * per) * 32;
-    if (threads > (vec ? 512 : 1024)) {
-        return launch_dense(k_gated_rows_long<DT>, grid, 1024, 0, 1, s, p);
-    }
-    const int per_sm = threads > 384 ? 1 : 2;
-    if (grid > per_sm * device_info().sm_count) grid = per_sm * device_info().sm_count;
+    const bool any = threads > (vec ? 512 : 1024);
+    const int grid = grad_rows_grid(a.T, threads > 384 && !any ? 1 : 2);
+    p.slots = grad_rows_slots(a.T, grid);
+    n_part = grid * p.slots;
+    if (any) return launch_dense(k_gated_rows_long<DT>, grid, 1024, 0, 1, s, p);
     if (vec)
         return per == 2 ? launch_dense(k_gated_rows<DT, 4, 2>, grid, threads, 0, 1, s, p)
                         : launch_dense(k_gated_rows<DT, 4, 4>, grid, threads, 0, 1, s, p);
@@ -637,7 +681,6 @@ cudaError_t launch_grad_rows(const GradRowsArgs& a, int* n_part, cudaStream_t s)
     p.scale = a.scale;
     p.partials = a.partials;
     p.done = a.done;
-    *n_part = grad_rows_grid(a.T);
     if (a.n_mats == 1)
         return a.dtype == MOE_F32    ? one_rows<MOE_F32>(a, p, s)
                : a.dtype == MOE_BF16 ? one_rows<MOE_BF16>(a, p, s)

@@ -138,3 +138,27 @@ def test_matmul_column_sums_of_a_long_batch(T, N, dtype):
     dh.check("ds", ds, want.cpu(), 36 * dh.U * want.cpu())
     want = T * dy[0].double()
     dh.check("dbias", db, want.cpu(), 36 * dh.U * want.cpu())
+
+
+# a group of columns a thread, four of them, rows of any length, single columns
+@pytest.mark.parametrize("T,N", [(300000, 64), (60000, 6400), (60000, 4099), (200000, 333), (9473, 2048), (5, 512)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_gated_column_sums_of_a_long_batch(T, N, dtype):
+    """The same for the scales of the gated block.  Bounds: the term's own error (dense_helpers), 31
+    additions in fp32, and what follows in fp64 but for one rounding a partial sum and one of the
+    result, 2u; 3u for the term's last products."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    K = 16
+    dy = (torch.rand(N, generator=gen, device="cuda") + 0.1).to(DT[dtype]).expand(T, N).contiguous()
+    acc = torch.randint(20_000, 200_000, (2, 1, N), generator=gen, device="cuda", dtype=torch.int32)
+    xd = torch.full((T,), 0.0123, device="cuda")
+    w = torch.randint(-127, 128, (N, K), generator=gen, device="cuda", dtype=torch.int8)
+    ss = [torch.full((N,), v, device="cuda") for v in (4e-4, 3e-4)]  # g up to 1, u up to 0.7
+    _, *got = moe.gated_ffn_backward(dy, acc.expand(2, T, N).contiguous(), xd, w, ss[0], w, ss[1])
+    d, x = dy[0].double(), xd[0].double() * acc[:, 0].double()
+    g, u = x[0] * ss[0].double(), x[1] * ss[1].double()
+    z, a, da, da_mag, _ = dh.act64("silu", g)
+    rel = (30 + 16 * z.abs()) * dh.U
+    for name, t, want, e in (("ds_gate", got[0], d * u * da * x[0], d * u * da_mag * rel * x[0]),
+                             ("ds_up", got[1], d * a * x[1], d * a * rel * x[1])):
+        dh.check(name, t, T * want.cpu(), T * (e + 36 * dh.U * want).cpu())
