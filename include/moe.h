@@ -385,7 +385,8 @@ enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1 };
  * dtype): d = amax/127 (fp32 IEEE divide), q = round-half-away-from-zero(x *
  * (1/d)) in [-127, 127]; a row with amax below 2^-112 stores d = 0, q = 0, and
  * a row that holds an infinity or a NaN stores d = NaN, q = 0.  Outputs
- * q [n_rows][cols] int8 (row stride ldq) and d [n_rows]. */
+ * q [n_rows][cols] int8 (row stride ldq) and d [n_rows].  cols up to 2^31 - 2^16,
+ * else MOE_EUNSUPPORTED. */
 int moe_quantize_act_token(const void *x, int dtype, int64_t n_rows, int cols, int64_t ldx, int8_t *q, int64_t ldq,
                            float *d, void *stream);
 

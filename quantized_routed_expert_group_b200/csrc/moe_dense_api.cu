@@ -11,6 +11,7 @@ namespace dense {
 
 constexpr int kMaxTokens = 1 << 28;
 constexpr int kMaxContraction = 131071;  // 128 * 128 * 131071 < 2^31
+constexpr int kMaxLength = 0x7FFF0000;   // kernels count columns and channels in int, up to a CTA's step past the end
 
 static bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 static size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
@@ -174,6 +175,7 @@ using namespace moe::dense;
 MOE_API int moe_quantize_act_token(const void* x, int dtype, int64_t n_rows, int cols, int64_t ldx, int8_t* q,
                                    int64_t ldq, float* d, void* stream) {
     if (n_rows < 0 || cols <= 0 || !known_type(dtype)) return MOE_EINVAL;
+    if (cols > kMaxLength) return MOE_EUNSUPPORTED;
     if (n_rows == 0) return MOE_OK;
     if (check_matrix(x, dtype, ldx, cols) || !q || ldq < cols || !d || !aligned(d, 4)) return MOE_EINVAL;
     return status_of(launch_quantize_token(x, dtype, n_rows, cols, ldx, q, ldq, d, (cudaStream_t)stream));
