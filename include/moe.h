@@ -364,9 +364,9 @@ int moe_get_device_error(void *workspace, void *stream, int32_t *code);
  * workspace where that pays and the workspace has room, and otherwise loaded as
  * they lie, which is slower.
  * T = 0 returns MOE_OK (gradients that sum over tokens are then set to zero).
- * T up to 2^28, contractions (cols; in a backward pass the number of matrices
- * times rows) up to 131071, so that every int32 sum is exact, else
- * MOE_EUNSUPPORTED.  The current device must be the one that holds the data.
+ * T up to 2^28, rows and cols up to 2^31 - 2^16, contractions (cols; in a
+ * backward pass the number of matrices times rows) up to 131071, so that every
+ * int32 sum is exact, else MOE_EUNSUPPORTED.  The current device must be the one that holds the data.
  * Results must not overlap inputs, the workspace or one another.  Calls may run
  * at the same time on several streams, each with its own results and workspace,
  * and may be captured into graphs.  Results do not depend on timing: equal calls

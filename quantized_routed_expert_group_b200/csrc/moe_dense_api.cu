@@ -31,7 +31,7 @@ struct NvtxRange {
 static int check_sizes(int T, int rows, int cols, int dtype) {
     if (T < 0 || rows <= 0 || cols <= 0) return MOE_EINVAL;
     if (!known_type(dtype)) return MOE_EINVAL;
-    if (T > kMaxTokens) return MOE_EUNSUPPORTED;
+    if (T > kMaxTokens || rows > kMaxLength || cols > kMaxLength) return MOE_EUNSUPPORTED;
     return MOE_OK;
 }
 
@@ -250,14 +250,15 @@ MOE_API int moe_gated_ffn(const int8_t* xq, int64_t ldx, const float* xd, int T,
 }
 
 MOE_API size_t moe_int8_forward_workspace_bytes(int n_mats, int T, int rows, int cols) {
-    if (n_mats < 1 || n_mats > kMaxMats || T < 0 || T > kMaxTokens || rows <= 0 || cols <= 0 || cols > kMaxContraction)
+    if (n_mats < 1 || n_mats > kMaxMats || T < 0 || T > kMaxTokens || rows <= 0 || rows > kMaxLength || cols <= 0 ||
+        cols > kMaxContraction)
         return 0;
     return forward_room(n_mats, T, rows, cols);
 }
 
 MOE_API size_t moe_int8_backward_workspace_bytes(int n_mats, int T, int rows, int cols, int dtype) {
     if (n_mats < 1 || n_mats > kMaxMats || T < 0 || T > kMaxTokens || rows <= 0 || cols <= 0 ||
-        (int64_t)n_mats * rows > kMaxContraction || !known_type(dtype))
+        cols > kMaxLength || (int64_t)n_mats * rows > kMaxContraction || !known_type(dtype))
         return 0;
     const size_t n = backward_layout(n_mats, T, rows, cols, dtype).total;
     return n ? n : 256;
