@@ -373,6 +373,7 @@ _ACTS = {"silu": 0, "gelu": 1}
 _ACT_TYPES = (torch.int8,)
 _CODE_TYPES = (torch.int8, torch.uint8)
 _ROW_TYPES = tuple(_DTYPES)
+_INT_MAX = 0x7FFFFFFF  # the library counts rows and columns in int (the quantiser its rows in 64 bits)
 
 
 def _refuse(t, dtypes, name: str, shape, dev: int):
@@ -385,20 +386,23 @@ def _refuse(t, dtypes, name: str, shape, dev: int):
         raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
     if dev >= 0 and t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    if max(t.shape) > _INT_MAX:
+        raise MoeError(MOE_EUNSUPPORTED, f"{name} of shape {tuple(t.shape)}")
     raise ValueError(f"{name} must be dense" if len(shape) != 2 else
                      f"{name} must have dense rows (last stride 1) that do not overlap")
 
 
-def _matrix(t: torch.Tensor, dtypes, name: str, rows: int = -1, cols: int = -1, dev: int = -1) -> int:
-    """Checks a 2-D operand (its rows, columns and device where they are given);
-    returns its row stride in elements."""
+def _matrix(t: torch.Tensor, dtypes, name: str, rows: int = -1, cols: int = -1, dev: int = -1,
+            most_rows: int = _INT_MAX) -> int:
+    """Checks a 2-D operand (its rows, columns and device where they are given,
+    and that its sizes fit the library's); returns its row stride in elements."""
     if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 2:
         (r, c), (ld, inner) = t.shape, t.stride()
         if r <= 1:
             ld = c
         d = t.get_device()
         if (d >= 0 and (d == dev or dev < 0) and (r == rows or rows < 0) and (c == cols or cols < 0)
-                and (inner == 1 or c <= 1) and ld >= c):
+                and (inner == 1 or c <= 1) and ld >= c and r <= most_rows and c <= _INT_MAX):
             return ld
     _refuse(t, dtypes, name, (rows, cols), dev)
 
@@ -445,7 +449,7 @@ def _on(dev: int, stream):
 def quantize_act_token(x: torch.Tensor, stream=None):
     """Rows of x [T][K] (fp32, bf16 or fp16) -> codes [T][K] int8 and scales [T]
     fp32 (see moe_quantize_act_token)."""
-    ld = _matrix(x, _ROW_TYPES, "x")
+    ld = _matrix(x, _ROW_TYPES, "x", most_rows=1 << 62)
     dev = x.get_device()
     if stream is not None or dev != _current_device():
         with _on(dev, stream):

@@ -1,6 +1,7 @@
 """The ends of the dense int8 operators' ranges, refused on the host (no GPU: the
 pointers are never dereferenced)."""
 import pytest
+import torch
 
 from quantized_routed_expert_group_b200 import build
 
@@ -45,3 +46,66 @@ def test_products_still_take_the_longest(L):
     """Sizes in range pass the checks: their workspace is given."""
     assert L.lib().moe_int8_forward_workspace_bytes(1, 17, LONGEST, 1001) > LONGEST * 1001
     assert L.lib().moe_int8_backward_workspace_bytes(1, 17, 32, LONGEST, 1) > 0
+
+
+# --- the binding, on tensors that have a shape and a device but no memory ---------------------------------
+class Calls:
+    """Stands in for the library: notes its calls, which all succeed."""
+
+    def __init__(self):
+        self.made = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.made.append((name, args))
+            return 256 if name.endswith("_bytes") else 0
+        return call
+
+
+@pytest.fixture
+def fake(L, monkeypatch):
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    calls = Calls()
+    monkeypatch.setattr(L, "lib", lambda: calls)
+    monkeypatch.setattr(L, "status_string", str)
+    monkeypatch.setattr(L, "_current_device", lambda: 0)
+    monkeypatch.setattr(L, "_raw_stream", lambda dev: 0)
+    with FakeTensorMode():
+        yield calls
+
+
+def t8(*shape):
+    return torch.empty(shape, dtype=torch.int8, device="cuda")
+
+
+def f32(*shape):
+    return torch.empty(shape, device="cuda")
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_binding_refuses_sizes_of_more_than_32_bits(L, fake):
+    """The library's sizes are 32-bit: 2^32 + 8 tokens would arrive there as 8."""
+    big = (1 << 32) + 8
+    for i, call in enumerate([
+            lambda: L.quantize_act_token(f32(1, big)),
+            lambda: L.int8_matmul(t8(big, 1), f32(big), t8(4, 1), f32(4)),
+            lambda: L.int8_matmul(t8(1, big), f32(1), t8(4, big), f32(4)),
+            lambda: L.int8_matmul(t8(1, 1), f32(1), t8(big, 1), f32(big)),
+            lambda: L.gated_ffn(t8(big, 1), f32(big), t8(4, 1), f32(4), t8(4, 1), f32(4)),
+            lambda: L.gated_ffn(t8(1, 1), f32(1), t8(big, 1), f32(big), t8(big, 1), f32(big)),
+            lambda: L.int8_matmul_backward(f32(big, 4), None, None, t8(4, 8), f32(4)),
+            lambda: L.int8_matmul_backward(f32(4, big), None, None, t8(big, 8), f32(big)),
+            lambda: L.int8_matmul_backward(f32(4, 4), None, None, t8(4, big), f32(4)),
+            lambda: L.gated_ffn_backward(f32(2, 4), torch.empty((2, 2, 4), dtype=torch.int32, device="cuda"), f32(2),
+                                         t8(4, big), f32(4), t8(4, big), f32(4)),
+            lambda: L.dense_ffn(f32(big, 4), L.ExpertBank(*(t8(1, 4, 4).view(torch.uint8) for _ in range(3)),
+                                                          *(f32(1, 4) for _ in range(3))))]):
+        with pytest.raises(L.MoeError) as e:
+            call()
+        assert e.value.status == EUNSUPPORTED and not fake.made, i
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_quantiser_takes_any_number_of_rows(L, fake):
+    q, d = L.quantize_act_token(f32((1 << 32) + 8, 1))
+    assert q.shape == ((1 << 32) + 8, 1) and fake.made[0][1][2] == (1 << 32) + 8
