@@ -469,7 +469,8 @@ def _room_bytes(n_mats: int, T: int, N: int, K: int) -> int:
 
 
 @functools.lru_cache(maxsize=1024)
-def _backward_bytes(n_mats: int, T: int, N: int, K: int, dtype: int) -> int:
+def _backward_bytes(dev: int, n_mats: int, T: int, N: int, K: int, dtype: int) -> int:
+    """(of the device `dev`, the current one: the size goes by its SMs)"""
     return lib().moe_int8_backward_workspace_bytes(n_mats, T, N, K, dtype)
 
 
@@ -531,7 +532,7 @@ def int8_matmul_backward(dy: torch.Tensor, acc: torch.Tensor | None, xd: torch.T
         db = s.new_empty(N)
     dt = _DTYPES[dy.dtype]
     dx = dy.new_empty(T, K)
-    size = _backward_bytes(1, T, N, K, dt)
+    size = _backward_bytes(dev, 1, T, N, K, dt)
     ws = w.new_empty(size, dtype=torch.uint8)
     st = lib().moe_int8_matmul_backward(dy.data_ptr(), dt, lddy, acc_p, xd_p, T, w.data_ptr(), ldw, s_p, N, K,
                                         dx.data_ptr(), K, None if ds is None else ds.data_ptr(),
@@ -591,7 +592,7 @@ def gated_ffn_backward(dh: torch.Tensor, acc: torch.Tensor, xd: torch.Tensor, w_
     dt, ac = _DTYPES[dh.dtype], _choice(act, _ACTS, "act")
     dx = dh.new_empty(T, K)
     dsg, dsu = s_gate.new_empty(N), s_up.new_empty(N)
-    size = _backward_bytes(2, T, N, K, dt)
+    size = _backward_bytes(dev, 2, T, N, K, dt)
     ws = w_gate.new_empty(size, dtype=torch.uint8)
     st = lib().moe_gated_ffn_backward(dh.data_ptr(), dt, lddh, acc_p, xd_p, T, w_gate.data_ptr(), ldg, sg_p,
                                       w_up.data_ptr(), ldu, su_p, N, K, ac, dx.data_ptr(), K, dsg.data_ptr(),

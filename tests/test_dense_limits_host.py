@@ -70,8 +70,12 @@ def fake(L, monkeypatch):
     monkeypatch.setattr(L, "status_string", str)
     monkeypatch.setattr(L, "_current_device", lambda: 0)
     monkeypatch.setattr(L, "_raw_stream", lambda dev: 0)
+    L._room_bytes.cache_clear()
+    L._backward_bytes.cache_clear()
     with FakeTensorMode():
         yield calls
+    L._room_bytes.cache_clear()  # what the stand-in answered is no size
+    L._backward_bytes.cache_clear()
 
 
 def t8(*shape):
@@ -109,3 +113,28 @@ def test_binding_refuses_sizes_of_more_than_32_bits(L, fake):
 def test_quantiser_takes_any_number_of_rows(L, fake):
     q, d = L.quantize_act_token(f32((1 << 32) + 8, 1))
     assert q.shape == ((1 << 32) + 8, 1) and fake.made[0][1][2] == (1 << 32) + 8
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_backward_workspace_is_sized_for_its_device(L, fake, monkeypatch):
+    """The gated backward's workspace grows with the device's SMs: a size asked for one device is not
+    taken for another."""
+    here = [0]
+    monkeypatch.setattr(L, "_current_device", lambda: here[0])
+    sent = []
+
+    def answer(self, name):
+        def call(*args):
+            if name.endswith("_bytes"):
+                return 1000 * (here[0] + 1)
+            sent.append(args[-2])  # the workspace's bytes
+            return 0
+        return call
+    monkeypatch.setattr(Calls, "__getattr__", answer)
+    for here[0] in (0, 1, 0):
+        def on(t):
+            return t.to(f"cuda:{here[0]}")
+        w, s = on(t8(12, 12)), on(f32(12))
+        L.gated_ffn_backward(on(f32(801, 12)), on(torch.empty((2, 801, 12), dtype=torch.int32, device="cuda")),
+                             on(f32(801)), w, s, w, s)
+    assert sent == [1000, 2000, 1000]
