@@ -366,7 +366,9 @@ def synth_bank(wl: synth.Workload, device, shared: bool = False, experts=None) -
 # with one fp32 scale each.  Matrices may be views whose rows are dense (last
 # stride 1) at any row stride.  The tensors of a call live on one device, which
 # need not be the current one; memory that a call allocates (results and
-# workspace) belongs to the stream that it runs on.
+# workspace) belongs to the stream that it runs on.  The calls record no gradients:
+# a tensor that requires one is refused unless gradients are switched off, as they
+# are in a torch.autograd.Function that joins a call and its backward pass.
 # ----------------------------------------------------------------------------
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _ACTS = {"silu": 0, "gelu": 1}
@@ -392,6 +394,13 @@ def _refuse(t, dtypes, name: str, shape, dev: int):
                      f"{name} must have dense rows (last stride 1) that do not overlap")
 
 
+def _no_gradient(name: str):
+    """Raises for an operand whose gradient would be recorded by an operator of torch's."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, and this call records none: call it under torch.no_grad() "
+                         "or in a torch.autograd.Function, with its backward pass")
+
+
 def _matrix(t: torch.Tensor, dtypes, name: str, rows: int = -1, cols: int = -1, dev: int = -1,
             most_rows: int = _INT_MAX) -> int:
     """Checks a 2-D operand (its rows, columns and device where they are given,
@@ -403,6 +412,8 @@ def _matrix(t: torch.Tensor, dtypes, name: str, rows: int = -1, cols: int = -1, 
         d = t.get_device()
         if (d >= 0 and (d == dev or dev < 0) and (r == rows or rows < 0) and (c == cols or cols < 0)
                 and (inner == 1 or c <= 1) and ld >= c and r <= most_rows and c <= _INT_MAX):
+            if t.requires_grad:
+                _no_gradient(name)
             return ld
     _refuse(t, dtypes, name, (rows, cols), dev)
 
@@ -415,6 +426,8 @@ def _vector(t: torch.Tensor, n: int, name: str, dev: int) -> int:
     if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 1 or t.numel() != n
             or t.get_device() != dev or not t.is_contiguous()):
         _refuse(t, _F32, name, (n,), dev)
+    if t.requires_grad:
+        _no_gradient(name)
     return t.data_ptr()
 
 
@@ -604,6 +617,8 @@ def gated_ffn_backward(dh: torch.Tensor, acc: torch.Tensor, xd: torch.Tensor, w_
 def _bank_part(t: torch.Tensor, dtype, name: str, shape, dev: int) -> int:
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"bank.{name} must be a contiguous {dtype} tensor {shape} on cuda:{dev} (one int8 expert)")
+    if t.requires_grad:
+        _no_gradient(f"bank.{name}")
     return t.data_ptr()
 
 

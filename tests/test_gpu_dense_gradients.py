@@ -162,3 +162,40 @@ def test_gated_column_sums_of_a_long_batch(T, N, dtype):
     for name, t, want, e in (("ds_gate", got[0], d * u * da * x[0], d * u * da_mag * rel * x[0]),
                              ("ds_up", got[1], d * a * x[1], d * a * rel * x[1])):
         dh.check(name, t, T * want.cpu(), T * (e + 36 * dh.U * want).cpu())
+
+
+class Linear(torch.autograd.Function):
+    """The product with its backward pass, as a program joins them."""
+
+    @staticmethod
+    def forward(ctx, x, w, s, bias):
+        q, d = moe.quantize_act_token(x)
+        y, acc = moe.int8_matmul(q, d, w, s, bias=bias, out_dtype=x.dtype, save=True)
+        ctx.save_for_backward(acc, d, w, s)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        dx, ds, dbias = moe.int8_matmul_backward(dy, *ctx.saved_tensors, bias_grad=True)
+        return dx, None, ds, dbias
+
+
+def test_an_autograd_function_of_the_calls():
+    """Leaves are refused outside, taken inside, and get the backward pass's gradients."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    T, K, N = 40, 96, 50
+    x = torch.randn((T, K), generator=gen, device="cuda").requires_grad_()
+    s = torch.rand(N, generator=gen, device="cuda").requires_grad_()
+    bias = torch.randn(N, generator=gen, device="cuda").requires_grad_()
+    w, dy = codes(gen, N, K), torch.randn((T, N), generator=gen, device="cuda")
+    with pytest.raises(ValueError, match="gradient"):
+        moe.quantize_act_token(x)
+    y = Linear.apply(x, w, s, bias)
+    y.backward(dy)
+    with torch.no_grad():
+        q, d = moe.quantize_act_token(x)
+        want, acc = moe.int8_matmul(q, d, w, s, bias=bias, save=True)
+        grads = moe.int8_matmul_backward(dy, acc, d, w, s, bias_grad=True)
+    assert torch.equal(y, want)
+    for leaf, g in zip((x, s, bias), grads):
+        assert torch.equal(leaf.grad, g)
