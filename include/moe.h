@@ -360,9 +360,9 @@ int moe_get_device_error(void *workspace, void *stream, int32_t *code);
  * at least the row's length; what lies between the rows is neither read nor
  * written); any number of rows and columns is supported within the limits
  * below, and any alignment that fits the element type.  Rows of codes whose
- * address or stride is no multiple of 16 bytes are copied to such ones in the
- * workspace where that pays and the workspace has room, and otherwise loaded as
- * they lie, which is slower.
+ * address or stride is no multiple of 16 bytes are slower: they are loaded as
+ * they lie, or, where their length is no multiple of 16 either, it pays and the
+ * workspace has room, copied to such ones first.
  * T = 0 returns MOE_OK (gradients that sum over tokens are then set to zero).
  * T up to 2^28, rows and cols up to 2^31 - 2^16, contractions (cols; in a
  * backward pass the number of matrices times rows) up to 131071, so that every
@@ -471,7 +471,8 @@ int moe_dense_ffn(const void *x, int dtype, int64_t ldx, int T, int hidden, int 
  * the current device since the last read (0 = none, 2 = a device-side wait ran
  * out; every wait is bounded by the GPU's global timer, 100 ms a pipeline
  * stage) into *code and clears it.  Returns MOE_OK when it is 0, MOE_EDEVICE
- * otherwise. */
+ * otherwise; the results of the products since the last read are unspecified
+ * then. */
 int moe_dense_device_error(void *stream, int32_t *code);
 
 /* Test hook of the failure-detection tests (the pages have no counterpart).

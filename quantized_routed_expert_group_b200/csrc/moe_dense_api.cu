@@ -44,10 +44,12 @@ static int check_matrix(const void* p, int dtype, int64_t ld, int cols) {
     return p && aligned(p, elem_size(dtype)) && ld >= cols ? MOE_OK : MOE_EINVAL;
 }
 
-// Copies of odd rows pay from 1.5 MB on: 333 x 1000 x 777 gated (1.9 MB) 17.9 ->
-// 11.4 us.  Below, the device saves less than the host spends on the launch (300 x
-// 1000 x 500 gated, 1.3 MB: 10.7 -> 8.5 us, and 3.5 us of the host), and the few
-// tokens that stream the weights gain nothing.
+// Copies of rows of an odd length pay from 1.5 MB on: 333 x 1000 x 777 gated (1.9
+// MB) 17.9 -> 11.4 us.  Below, the device saves less than the host spends on the
+// launch (300 x 1000 x 500 gated, 1.3 MB: 10.7 -> 8.5 us, and 3.5 us of the host;
+// only a program that replays a graph would gain), and the few tokens that stream
+// the weights gain nothing.  The sizes of workspaces know the rows' length alone:
+// rows of a multiple of 16 codes at other addresses or strides are never copied.
 constexpr size_t kCopyBytes = 3u << 19;
 
 static size_t forward_room(int n_mats, int T, int rows, int cols) {

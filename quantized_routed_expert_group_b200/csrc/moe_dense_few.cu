@@ -15,11 +15,13 @@
 // shared memory, with the arithmetic of k_quantize_token, while its first
 // weights are under way; that saves a launch and a trip through L2.
 //
-// Bound by the weights' way from L2 and HBM, and by the launch.  Three CTAs of 8
-// warps an SM where there are rows for them (16 tokens through 2048 x 6144: 3.9
-// us, against 6.6 us with one), one CTA of 16 warps otherwise (one token through
-// 6144 x 2048: 2.8 us, 4.5 TB/s; the gated block 7.0 us, 3.6 TB/s, with weights
-// partly out of HBM).
+// Bound by the weights' way from L2 or HBM, and by the launch.  Three CTAs of 8
+// warps an SM where there are rows for them (16 tokens through 2048 x 6144: 3.8
+// us with the weights in L2, against 6.6 us with one; 5.0 us with the weights in
+// HBM), one CTA of 16 warps otherwise (one token through 6144 x 2048: 2.8 us with
+// the weights in L2, 4.1 us, 3.1 TB/s, in HBM; the gated block 6.8 and 8.1 us, 3.1
+// TB/s).  The bound of three CTAs leaves the quantising form 80 registers, and it
+// spills 140 bytes a thread.
 #include <type_traits>
 
 #include "moe_dense.cuh"

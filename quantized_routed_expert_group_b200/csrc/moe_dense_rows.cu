@@ -229,9 +229,10 @@ __device__ __forceinline__ float fixed_point(uint32_t m, float& lift, RowScale& 
 }
 
 // Rows of one matrix: v = dy s, read once and kept in registers until the row's
-// largest value is known.  Bound by latency and issue (48 % of the issue slots at
-// 2048 x 6144 bf16, 14.3 us with the rows in HBM: 25 MB read at 22 % of the
-// memory's rate; the planes stay in L2 for the product).
+// largest value is known.  Bound by latency and issue (52 % of the issue slots at
+// 2048 x 6144 bf16, 16.3 us with the rows in HBM: 25 MB read at 19 % of the
+// memory's rate; the planes stay in L2 for the product).  The fp32 form spills 80
+// bytes a thread.
 constexpr int kRowCache = 6;
 
 template <int DT, int VEC>
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(32 * kDotsWarps, 4) k_col_dots(const ColDotsPa
 // saved sums, and the CTA's part of the scales' gradients, which are column sums
 // over its rows.  A thread owns NJ groups of VEC columns; the next row's loads are
 // in flight while a row waits for its largest value.  Bound by the arithmetic and
-// its latency: 2048 x 2048 bf16 22 us, 42 MB from HBM at 23 % of its rate, 42 % of
+// its latency: 2048 x 2048 bf16 22 us, 42 MB from HBM at 24 % of its rate, 44 % of
 // the issue slots (two CTAs an SM; three and four were slower).
 template <int DT, int VEC, int NJ>
 __global__ void __launch_bounds__(VEC == 1 ? 1024 : 512) k_gated_rows(const GradRowsParams p) {
@@ -637,7 +638,9 @@ static cudaError_t grad_rows(const GradRowsArgs& a, GradRowsParams p, int& n_par
     const int groups = vec ? a.N / 4 : a.N;
     // two groups of four columns a thread, four beyond 4096 columns; single columns
     // one or four.  Two CTAs an SM without spills beat three with them (2048
-    // columns: 123.0 against 125.8 us of the training step at 2048 tokens).
+    // columns: 123.0 against 125.8 us of the training step at 2048 tokens, measured
+    // with two planes).  Four groups of four columns do spill, 216 to 336 bytes a
+    // thread.
     const int per = vec ? (groups <= 2 * 512 ? 2 : 4) : (groups <= 512 ? 1 : 4);
     const int threads = (groups + 32 * per - 1) / (32 * per) * 32;
     const bool any = threads > (vec ? 512 : 1024);

@@ -655,7 +655,8 @@ def dense_ffn(x: torch.Tensor, bank: ExpertBank, act: str = "silu", out: torch.T
 
 def dense_device_error(stream=None) -> int:
     """The fault code that a dense product recorded on the current device (0 =
-    none), cleared by reading; synchronises the stream."""
+    none; otherwise the results of the products since the last read are
+    unspecified), cleared by reading; synchronises the stream."""
     code = ctypes.c_int32(0)
     st = lib().moe_dense_device_error(_stream(stream), ctypes.byref(code))
     if st not in (MOE_OK, MOE_EDEVICE):
